@@ -50,7 +50,7 @@ PEAK_FP4_TFLOPS = 10100.0          # MI355X dense MXFP4 MFMA (published)
 PEAK_HBM_GBS = 8000.0              # MI355X HBM3E (published)
 METRIC = "dual-branch W4A4 FFN GEMM effective TFLOPS, % MXFP4 MFMA peak (480p/720p)"
 TRAFFIC_FILE = os.path.join(ROOT, "profiles", "dual_gemm_ffn0_480p_traffic.json")
-# the dual GEMM's sources: its kernel file and the headers it includes
+# the dual GEMM's sources: its kernel file and the headers that its bf16 output is built from
 GEMM_SRCS = [os.path.join(ROOT, "mixed_gemm_amd", "csrc", f) for f in ("k_gemm.hip", "mg_device.h", "mg_internal.h")]
 
 

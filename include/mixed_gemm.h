@@ -322,6 +322,119 @@ int mg_gelu_quantize_act(const mg_plan* p, const uint16_t* Y, int64_t M, const m
 int mg_dual_gemm_gelu_quant(const mg_plan* p0, const mg_act* a0, int64_t M, const mg_plan* p2, const mg_act* a2,
                             hipStream_t stream);
 
+/* ---- around the block: the norm ahead of it with its modulation, the bias
+ * and activation of its projections, the gated residual after it (and the
+ * norm after it).  The FFN block of the diffusion transformer the layer is
+ * for runs as
+ *     h = norm(x) (1 + scale) + shift;  x = x + gate * ffn(h)
+ * with shift, scale and gate made from the time step, one row per sample (or
+ * per token).  Sums, statistics and all arithmetic are in f32; every result
+ * is rounded once, to nearest even, to the type it is stored in.  In these
+ * calls X, Y, O, H are rows `ld` elements apart (ld >= their width) that only
+ * need their element's alignment; finite inputs are not required: NaN and
+ * infinities spread as the formulas say, except that padding rows take
+ * nothing from their inputs (below). ---- */
+
+typedef enum { MG_NORM_LAYER = 0, MG_NORM_RMS = 1 } mg_norm_kind;
+
+/* n_j = (x_j - mean) / sqrt(var + eps) w_j + b_j with the row's mean and
+ * (biased) variance (MG_NORM_LAYER), or x_j / sqrt(mean x^2 + eps) w_j + b_j
+ * (MG_NORM_RMS).  weight, bias [K] of type dtype (MG_F32 or MG_BF16), either
+ * may be NULL (1, 0); eps >= 0. */
+typedef struct {
+    const void* weight;
+    const void* bias;
+    int32_t dtype;
+    int32_t kind;
+    double eps;
+} mg_norm;
+
+/* Modulation rows: scale, shift, gate are [rows][width] matrices of type
+ * dtype whose rows are ld elements apart (three column ranges of one matrix,
+ * for instance); each may be NULL (0, 0, 1).  Token row r uses modulation row
+ * i(r) = index[r], or r / group when index is NULL (then the M token rows
+ * must not run past `rows` groups).  An index outside [0, rows) marks a
+ * padding token: its norm output is 0 whatever its input holds, and a
+ * residual passes it through unchanged. */
+typedef struct {
+    const void* scale;
+    const void* shift;
+    const void* gate;
+    const int32_t* index;
+    int64_t group;
+    int64_t ld;
+    int32_t rows;
+    int32_t dtype;
+} mg_mod;
+
+/* H[r] = n (1 + scale_i(r)) + shift_i(r), n the norm of X[r], r < M; K <= 65536
+ * channels.  mod may be NULL (H = n).  H may be X where type and ld agree;
+ * M == 0 is a no-op. */
+int mg_norm_mod(const mg_norm* norm, const mg_mod* mod, const void* X, int32_t dtype, int64_t ldx, int64_t M,
+                int32_t K, void* H, int32_t h_dtype, int64_t ldh, hipStream_t stream);
+
+/* The residual after a block, and the norm ahead of the next one in the same
+ * pass: O[r] = X[r] + gate_i(r) p(Y[r]), p the norm `post` of the block's
+ * output or nothing (post NULL); and, where norm is given, H[r] = the
+ * norm-and-modulation of that sum (before it is rounded to O's type) with
+ * norm and mod as in mg_norm_mod.  O has X's type; gate (its `gate` rows and
+ * i(r)) and mod may be NULL.  O may be X, and H may be Y, where type and ld
+ * agree. */
+typedef struct {
+    const void* X;
+    const void* Y;
+    void* O;
+    void* H;              /* NULL where norm is NULL */
+    int64_t ldx, ldy, ldo, ldh;
+    int32_t dtype;        /* of X and O */
+    int32_t y_dtype, h_dtype;
+    int32_t reserved;     /* 0 */
+    const mg_mod* gate;
+    const mg_norm* post;
+    const mg_norm* norm;
+    const mg_mod* mod;
+} mg_residual;
+int mg_residual_norm(const mg_residual* a, int64_t M, int32_t K, hipStream_t stream);
+
+/* mg_norm_mod into bf16 and mg_quantize_act of the result in one pass: the
+ * operands of the projection behind the norm, bit for bit what those two
+ * calls write (pads included), without writing the normalized rows.
+ * K = p->d.K. */
+int mg_norm_quantize_act(const mg_plan* p, const mg_norm* norm, const mg_mod* mod, const void* X, int32_t dtype,
+                         int64_t ldx, int64_t M, const mg_act* a, hipStream_t stream);
+
+typedef enum { MG_ACT_NONE = 0, MG_ACT_GELU_TANH = 1, MG_ACT_SILU = 2 } mg_act_fn;
+
+/* Epilogue of the dual GEMM on its fp32 sums v[m][n]:
+ *     v += bias[n];  v = act(v);  Y = residual[m][n] + gate_i(m)[n] v
+ * with bias [N] of bias_dtype or NULL, mod's gate rows and i(m) as above (mod
+ * NULL: gate 1; only its gate is used), residual rows ldr elements apart of
+ * residual_dtype, or NULL (0).  A padding row gets Y = residual (0 without
+ * one).  GELU-tanh and SiLU are evaluated in f32 with the hardware exp2 and
+ * reciprocal.  Bases must be 16-byte aligned, ld of the residual and of the
+ * gate rows a multiple of 8 elements, else MG_ERR_ALIGN.  Y may be the
+ * residual (same type, ldr == N). */
+typedef struct {
+    const void* bias;
+    const void* residual;
+    const mg_mod* mod;
+    int64_t ldr;
+    int32_t bias_dtype;
+    int32_t residual_dtype;
+    int32_t act;          /* mg_act_fn */
+    int32_t reserved;     /* 0 */
+} mg_epilogue;
+
+/* mg_dual_gemm with the epilogue above; e may be NULL.  The order of the fp32
+ * sums may differ from mg_dual_gemm's (few rows take a kernel of their own
+ * that splits K), but is fixed: the same call gives the same bits. */
+int mg_dual_gemm_ep(const mg_plan* p, const mg_act* a, int64_t M, const mg_epilogue* e, void* Y, int32_t y_dtype,
+                    hipStream_t stream);
+
+/* mg_quantize_act followed by mg_dual_gemm_ep. */
+int mg_forward_ep(const mg_plan* p, const void* X, int32_t dtype, int64_t M, const mg_act* a, const mg_epilogue* e,
+                  void* Y, int32_t y_dtype, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

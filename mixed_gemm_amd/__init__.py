@@ -30,6 +30,10 @@ MG_W_1X32, MG_W_32X32, MG_W_128X1 = 0, 1, 2
 LAYOUTS = {"1x32": MG_W_1X32, "32x32": MG_W_32X32, "128x1": MG_W_128X1}
 MG_SCORE_MAX, MG_SCORE_SMOOTHED = 0, 1
 SCORES = {"max": MG_SCORE_MAX, "smoothed": MG_SCORE_SMOOTHED}
+MG_NORM_LAYER, MG_NORM_RMS = 0, 1
+NORMS = {"layer": MG_NORM_LAYER, "rms": MG_NORM_RMS}
+MG_ACT_NONE, MG_ACT_GELU_TANH, MG_ACT_SILU = 0, 1, 2
+ACTS = {"none": MG_ACT_NONE, "gelu": MG_ACT_GELU_TANH, "silu": MG_ACT_SILU}
 
 STATUS = {0: "MG_OK", -1: "MG_ERR_ARG", -2: "MG_ERR_SHAPE", -3: "MG_ERR_DTYPE", -4: "MG_ERR_ALIGN",
           -5: "MG_ERR_UNSUPPORTED", -6: "MG_ERR_HIP"}
@@ -62,11 +66,37 @@ class mg_pct(ctypes.Structure):
                 ("reserved", ctypes.c_int32)]
 
 
+class mg_norm(ctypes.Structure):
+    _fields_ = [("weight", ctypes.c_void_p), ("bias", ctypes.c_void_p), ("dtype", ctypes.c_int32),
+                ("kind", ctypes.c_int32), ("eps", ctypes.c_double)]
+
+
+class mg_mod(ctypes.Structure):
+    _fields_ = [("scale", ctypes.c_void_p), ("shift", ctypes.c_void_p), ("gate", ctypes.c_void_p),
+                ("index", ctypes.c_void_p), ("group", ctypes.c_int64), ("ld", ctypes.c_int64),
+                ("rows", ctypes.c_int32), ("dtype", ctypes.c_int32)]
+
+
+class mg_residual(ctypes.Structure):
+    _fields_ = [("X", ctypes.c_void_p), ("Y", ctypes.c_void_p), ("O", ctypes.c_void_p), ("H", ctypes.c_void_p),
+                ("ldx", ctypes.c_int64), ("ldy", ctypes.c_int64), ("ldo", ctypes.c_int64), ("ldh", ctypes.c_int64),
+                ("dtype", ctypes.c_int32), ("y_dtype", ctypes.c_int32), ("h_dtype", ctypes.c_int32),
+                ("reserved", ctypes.c_int32), ("gate", ctypes.POINTER(mg_mod)), ("post", ctypes.POINTER(mg_norm)),
+                ("norm", ctypes.POINTER(mg_norm)), ("mod", ctypes.POINTER(mg_mod))]
+
+
+class mg_epilogue(ctypes.Structure):
+    _fields_ = [("bias", ctypes.c_void_p), ("residual", ctypes.c_void_p), ("mod", ctypes.POINTER(mg_mod)),
+                ("ldr", ctypes.c_int64), ("bias_dtype", ctypes.c_int32), ("residual_dtype", ctypes.c_int32),
+                ("act", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
 EXPORTS = ("mg_version", "mg_last_error", "mg_plan_bytes", "mg_act_bytes", "mg_calib_reset",
            "mg_calib_act", "mg_weight_range", "mg_smooth_scales", "mg_outlier_set", "mg_fold_pack",
            "mg_plan_build", "mg_quantize_act", "mg_dual_gemm", "mg_forward", "mg_gelu_tanh_bf16",
            "mg_gelu_quantize_act", "mg_pct_reset", "mg_pct_count", "mg_pct_select", "mg_quantize_act_stats",
-           "mg_forward_noalloc", "mg_dual_gemm_gelu_quant")
+           "mg_forward_noalloc", "mg_dual_gemm_gelu_quant", "mg_norm_mod", "mg_residual_norm",
+           "mg_norm_quantize_act", "mg_dual_gemm_ep", "mg_forward_ep")
 
 _lib = None
 
@@ -103,6 +133,12 @@ def lib() -> ctypes.CDLL:
             "mg_pct_reset": ([P(mg_pct), vp], ctypes.c_int),
             "mg_pct_count": ([P(mg_pct), i32, vp, i64, vp], ctypes.c_int),
             "mg_pct_select": ([P(mg_pct), i32, ctypes.c_double, vp, vp], ctypes.c_int),
+            "mg_norm_mod": ([P(mg_norm), P(mg_mod), vp, i32, i64, i64, i32, vp, i32, i64, vp], ctypes.c_int),
+            "mg_residual_norm": ([P(mg_residual), i64, i32, vp], ctypes.c_int),
+            "mg_norm_quantize_act": ([P(mg_plan), P(mg_norm), P(mg_mod), vp, i32, i64, i64, P(mg_act), vp],
+                                     ctypes.c_int),
+            "mg_dual_gemm_ep": ([P(mg_plan), P(mg_act), i64, P(mg_epilogue), vp, i32, vp], ctypes.c_int),
+            "mg_forward_ep": ([P(mg_plan), vp, i32, i64, P(mg_act), P(mg_epilogue), vp, i32, vp], ctypes.c_int),
         }
         missing = set(EXPORTS) - set(sig)
         if missing:                       # an undeclared signature would truncate 64-bit pointers
@@ -471,6 +507,185 @@ def mg_pct_select(st: PctState, pass_: int, q: float, score: torch.Tensor | None
         _vec(score, st.K, "score")
     c = st.c()
     _check(lib().mg_pct_select(ctypes.byref(c), pass_, float(q), _ptr(score), _stream(stream)))
+
+
+# ----------------------------------------------------------------------------- around the block
+
+def _ref(x):
+    """The C struct of a Norm, Mod or Epilogue (None: a null pointer)."""
+    return None if x is None else ctypes.byref(x.c)
+
+
+def _rows(t: torch.Tensor, name: str, cols: int | None = None) -> tuple[int, int]:
+    """Rows of consecutive elements at any distance: (rows, elements between rows)."""
+    M, K = _matrix(t, name, cols)
+    _need(t.is_cuda, f"{name}: device tensor expected")
+    _need(K <= 1 or t.stride(1) == 1, f"{name}: the elements of a row must be consecutive, got strides {t.stride()}")
+    ld = t.stride(0) if M > 1 else max(K, t.stride(0))
+    _need(ld >= K, f"{name}: rows must not overlap, got strides {t.stride()}")
+    return M, ld
+
+
+class Norm:
+    """A norm (the C header's mg_norm): kind "layer" or "rms", weight and bias
+    [K] (float32 or bf16, or None).  Holds the tensors it was made from."""
+
+    def __init__(self, kind: str = "layer", weight: torch.Tensor | None = None, bias: torch.Tensor | None = None,
+                 eps: float = 1e-6):
+        _need(kind in NORMS, f"kind must be one of {sorted(NORMS)}, got {kind!r}")
+        self.width = None
+        for t, n in ((weight, "weight"), (bias, "bias")):
+            if t is not None:
+                _need(t.dim() == 1 and t.is_cuda and t.is_contiguous(), f"{n} must be a contiguous device vector")
+                _need(self.width in (None, t.shape[0]), "weight and bias must have the same length")
+                self.width = int(t.shape[0])
+        if weight is not None and bias is not None:
+            _need(_dtype(weight) == _dtype(bias), "weight and bias must have the same type")
+        self.weight, self.bias = weight, bias
+        t = weight if weight is not None else bias
+        self.c = mg_norm(_ptr(weight), _ptr(bias), MG_F32 if t is None else _dtype(t), NORMS[kind], float(eps))
+
+
+class Mod:
+    """Modulation rows (the C header's mg_mod): scale, shift, gate [rows][width]
+    (float32 or bf16, equal types and row distances; each may be None), and the
+    modulation row of token r: index[r] (int32, outside [0, rows): a padding
+    token) or r // group (default: one row for all tokens)."""
+
+    def __init__(self, scale: torch.Tensor | None = None, shift: torch.Tensor | None = None,
+                 gate: torch.Tensor | None = None, index: torch.Tensor | None = None, group: int | None = None,
+                 rows: int | None = None):
+        self.width, dtype, ld = None, MG_F32, 0
+        for t, n in ((scale, "scale"), (shift, "shift"), (gate, "gate")):
+            if t is None:
+                continue
+            r, d = _rows(t, n)
+            _need(rows in (None, r), f"{n} has {r} rows, expected {rows}")
+            _need(self.width is None or (self.width, dtype) == (t.shape[1], _dtype(t)),
+                  "scale, shift and gate must have the same width and type")
+            _need(self.width is None or r == 1 or d == ld, "scale, shift and gate rows must be equally far apart")
+            rows, self.width, dtype, ld = r, int(t.shape[1]), _dtype(t), d
+        _need(rows is not None, "a modulation without tensors needs its number of rows")
+        self.tokens = None
+        if index is not None:
+            _need(index.dim() == 1 and index.dtype == torch.int32 and index.is_cuda and index.is_contiguous(),
+                  "index must be a contiguous int32 device vector")
+            _need(group is None, "give either index or group")
+            self.tokens = int(index.shape[0])
+        self.tensors = (scale, shift, gate, index)
+        ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
+        self.c = mg_mod(ptr(scale), ptr(shift), ptr(gate), _ptr(index), (1 << 62) if group is None else int(group),
+                        ld, rows, dtype)
+
+
+def _check_norm(n: Norm | None, K: int, name: str) -> None:
+    if n is not None:
+        _need(isinstance(n, Norm), f"{name} must be a Norm")
+        _need(n.width in (None, K), f"{name} is for {n.width} channels, the rows have {K}")
+
+
+def _check_mod(m: Mod | None, M: int, K: int, name: str) -> None:
+    if m is not None:
+        _need(isinstance(m, Mod), f"{name} must be a Mod")
+        _need(m.width in (None, K), f"{name} is for {m.width} channels, the rows have {K}")
+        _need(m.tokens in (None, M), f"{name} has an index of {m.tokens} tokens, the input has {M} rows")
+
+
+class Epilogue:
+    """Epilogue of a projection (the C header's mg_epilogue): bias [N], act
+    "none", "gelu" or "silu", gate (a Mod with gate rows [rows][N]), residual
+    [M][N]; each may be None."""
+
+    def __init__(self, bias: torch.Tensor | None = None, act: str = "none", gate: Mod | None = None,
+                 residual: torch.Tensor | None = None):
+        _need(act in ACTS, f"act must be one of {sorted(ACTS)}, got {act!r}")
+        if bias is not None:
+            _need(bias.dim() == 1 and bias.is_cuda and bias.is_contiguous(), "bias must be a contiguous device vector")
+        ldr = _rows(residual, "residual")[1] if residual is not None else 0
+        self.bias, self.gate, self.residual = bias, gate, residual
+        self.c = mg_epilogue(_ptr(bias), None if residual is None else residual.data_ptr(),
+                             None if gate is None else ctypes.pointer(gate.c), ldr,
+                             MG_F32 if bias is None else _dtype(bias),
+                             MG_F32 if residual is None else _dtype(residual), ACTS[act], 0)
+
+    def check(self, M: int, N: int) -> None:
+        _need(self.bias is None or self.bias.shape[0] == N, f"bias must have {N} elements")
+        _check_mod(self.gate, M, N, "gate")
+        _need(self.residual is None or tuple(self.residual.shape) == (M, N), f"residual must be [{M}][{N}]")
+
+
+def mg_norm_mod(norm: Norm, mod: Mod | None, X: torch.Tensor, H: torch.Tensor, stream=None) -> None:
+    """H = norm(X) (1 + scale) + shift; X and H may have rows at any distance."""
+    M, ldx = _rows(X, "X")
+    K = X.shape[1]
+    Mh, ldh = _rows(H, "H", K)
+    _need(Mh == M, f"H must have {M} rows, got {Mh}")
+    _check_norm(norm, K, "norm")
+    _check_mod(mod, M, K, "mod")
+    _check(lib().mg_norm_mod(_ref(norm), _ref(mod), X.data_ptr(), _dtype(X), ldx, M, K, H.data_ptr(), _dtype(H), ldh,
+                             _stream(stream)))
+
+
+def mg_residual_norm(X: torch.Tensor, Y: torch.Tensor, O: torch.Tensor, gate: Mod | None = None,
+                     post: Norm | None = None, norm: Norm | None = None, mod: Mod | None = None,
+                     H: torch.Tensor | None = None, stream=None) -> None:
+    """O = X + gate * post(Y) and, with norm, H = norm(O) (1 + scale) + shift of
+    the unrounded sum; any row distances."""
+    M, ldx = _rows(X, "X")
+    K = X.shape[1]
+    My, ldy = _rows(Y, "Y", K)
+    Mo, ldo = _rows(O, "O", K)
+    _need(My == M and Mo == M, f"Y and O must have {M} rows, got {My} and {Mo}")
+    _need(_dtype(O) == _dtype(X), "O must have X's type")
+    _need((norm is None) == (H is None), "H goes with norm")
+    _need(norm is not None or mod is None, "mod goes with norm")
+    ldh, h, h_dtype = 0, None, MG_BF16
+    if H is not None:
+        Mh, ldh = _rows(H, "H", K)
+        _need(Mh == M, f"H must have {M} rows, got {Mh}")
+        h, h_dtype = H.data_ptr(), _dtype(H)
+    _check_norm(post, K, "post")
+    _check_norm(norm, K, "norm")
+    _check_mod(gate, M, K, "gate")
+    _check_mod(mod, M, K, "mod")
+    ptr = lambda x: None if x is None else ctypes.pointer(x.c)  # noqa: E731
+    a = mg_residual(X.data_ptr(), Y.data_ptr(), O.data_ptr(), h, ldx, ldy, ldo, ldh, _dtype(X), _dtype(Y), h_dtype, 0,
+                    ptr(gate), ptr(post), ptr(norm), ptr(mod))
+    _check(lib().mg_residual_norm(ctypes.byref(a), M, K, _stream(stream)))
+
+
+def mg_norm_quantize_act(plan: Plan, norm: Norm, mod: Mod | None, X: torch.Tensor, act: Act, stream=None) -> None:
+    """mg_norm_mod into bf16, then mg_quantize_act, in one pass (the same bits)."""
+    M, ldx = _rows(X, "X", plan.desc.K)
+    _check_act(plan.desc, act, M)
+    _check_norm(norm, plan.desc.K, "norm")
+    _check_mod(mod, M, plan.desc.K, "mod")
+    p, a = plan.c(), act.c()
+    _check(lib().mg_norm_quantize_act(ctypes.byref(p), _ref(norm), _ref(mod), X.data_ptr(), _dtype(X), ldx, M,
+                                      ctypes.byref(a), _stream(stream)))
+
+
+def mg_dual_gemm_ep(plan: Plan, act: Act, ep: Epilogue | None, Y: torch.Tensor, stream=None) -> None:
+    """mg_dual_gemm with bias, activation, gate and residual in its epilogue."""
+    _check_act(plan.desc, act)
+    _check_y(plan.desc, Y, act.M)
+    if ep is not None:
+        ep.check(act.M, plan.desc.N)
+    p, a = plan.c(), act.c()
+    _check(lib().mg_dual_gemm_ep(ctypes.byref(p), ctypes.byref(a), act.M, _ref(ep), _ptr(Y), _dtype(Y),
+                                 _stream(stream)))
+
+
+def mg_forward_ep(plan: Plan, X: torch.Tensor, act: Act, ep: Epilogue | None, Y: torch.Tensor, stream=None) -> None:
+    """mg_quantize_act, then mg_dual_gemm_ep."""
+    M, _ = _matrix(X, "X", plan.desc.K)
+    _check_act(plan.desc, act, M)
+    _check_y(plan.desc, Y, M)
+    if ep is not None:
+        ep.check(M, plan.desc.N)
+    p, a = plan.c(), act.c()
+    _check(lib().mg_forward_ep(ctypes.byref(p), _ptr(X), _dtype(X), M, ctypes.byref(a), _ref(ep), _ptr(Y), _dtype(Y),
+                               _stream(stream)))
 
 
 # ----------------------------------------------------------------------------- convenience

@@ -23,6 +23,8 @@
 #include <type_traits>
 #include <utility>
 
+#include "gemm_epilogue.h"
+#include "mg_block.h"
 #include "mg_device.h"
 #include "mg_internal.h"
 
@@ -169,6 +171,18 @@ struct GemmArgs {
     uint8_t* As2;
     uint8_t* XO2;
     int32_t k2;
+    EpArgs ep;          // bias, activation, gate and residual (EpOut)
+};
+
+// Output tag of the epilogue with bias, activation, gate and residual, writing
+// Y as T (float, or uint16_t for bf16).
+template <typename T>
+struct EpOut {};
+template <typename T>
+struct IsEp : std::false_type {};
+template <typename T>
+struct IsEp<EpOut<T>> : std::true_type {
+    using type = T;
 };
 
 // Output tag of the epilogue that applies GELU to the bf16-rounded tile and
@@ -736,6 +750,8 @@ dual_gemm_tiled(GemmArgs g) {
             // every wave's staging reads are done (their data fed the stores
             // above) before the next copies reuse the slots
             __builtin_amdgcn_s_barrier();
+        } else if constexpr (IsEp<OutT>::value) {
+            ep_store<typename IsEp<OutT>::type, JB>(g.ep, g.Y, acc, o.m0 + wm * 128, o.n0 + wn * 32 * JB, M, N, l32, h);
         } else {
             // fp32: four consecutive columns per register group -> 16-byte stores
             float* Yf = static_cast<float*>(g.Y);
@@ -849,7 +865,7 @@ hipError_t launch_dual_gemm(const uint8_t* Aq, const uint8_t* As, const uint16_t
                             hipStream_t st) {
     if (M <= 0) return hipSuccess;
     GemmArgs a{Aq, As, XO, Wq, Ws, WO, Y, M, N, K, k, (int32_t)((M + TBM - 1) / TBM), (N + TBN - 1) / TBN,
-               nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, 0};
+               nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, 0, EpArgs{}};
     return y_dtype == MG_BF16 ? launch_tiled<uint16_t>(a, st) : launch_tiled<float>(a, st);
 }
 
@@ -868,8 +884,17 @@ hipError_t launch_dual_gemm_gelu_quant(const uint8_t* Aq, const uint8_t* As, con
     hipError_t e = launch_fill_u32(reinterpret_cast<uint32_t*>(As2), 0u, sc_bytes(M, N) / 4, st);
     if (e != hipSuccess) return e;
     GemmArgs a{Aq, As, XO, Wq, Ws, WO, nullptr, M, N, K, k, (int32_t)((M + TBM - 1) / TBM), (N + TBN - 1) / TBN,
-               s2, rcp2, pos2, Aq2, As2, reinterpret_cast<uint8_t*>(XO2), k2};
+               s2, rcp2, pos2, Aq2, As2, reinterpret_cast<uint8_t*>(XO2), k2, EpArgs{}};
     return launch_tiled<QuantOut>(a, st);
+}
+
+hipError_t launch_dual_gemm_ep(const uint8_t* Aq, const uint8_t* As, const uint16_t* XO, const uint8_t* Wq,
+                               const uint8_t* Ws, const uint16_t* WO, int64_t M, int32_t N, int32_t K, int32_t k,
+                               const EpArgs& e, void* Y, int32_t y_dtype, hipStream_t st) {
+    if (M <= 0) return hipSuccess;
+    GemmArgs a{Aq, As, XO, Wq, Ws, WO, Y, M, N, K, k, (int32_t)((M + TBM - 1) / TBM), (N + TBN - 1) / TBN,
+               nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, 0, e};
+    return y_dtype == MG_BF16 ? launch_tiled<EpOut<uint16_t>>(a, st) : launch_tiled<EpOut<float>>(a, st);
 }
 
 }  // namespace mg

@@ -22,13 +22,11 @@ int hip_fail(hipError_t e, const char* where) {
     return fail(MG_ERR_HIP, "%s: %s", where, hipGetErrorString(e));
 }
 
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+}  // namespace
 
-#define MG_CHECK_PTR(p, name)                                                       \
-    do {                                                                            \
-        if ((p) == nullptr) return fail(MG_ERR_ARG, "%s: null pointer", name);      \
-        if (!aligned16(p)) return fail(MG_ERR_ALIGN, "%s: not 16-byte aligned", name); \
-    } while (0)
+namespace mg {
+
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 
 int check_dtype(int32_t dtype) {
     if (dtype != MG_F32 && dtype != MG_BF16) return fail(MG_ERR_DTYPE, "dtype %d is not MG_F32/MG_BF16", dtype);
@@ -91,10 +89,6 @@ int check_act(const mg_plan* p, const mg_act* a) {
     return MG_OK;
 }
 
-}  // namespace
-
-namespace mg {
-
 int check_forward(const mg_plan* p, const void* X, int32_t dtype, int64_t M, const void* Y, int32_t y_dtype) {
     if (int e = check_plan(p, true)) return e;
     if (int e = check_dtype(dtype)) return e;
@@ -145,9 +139,11 @@ int device_cu_count() {
 
 }  // namespace mg
 
+using namespace mg;
+
 extern "C" {
 
-int mg_version(void) { return 400; }   // 0.4.0: operands in fragment order
+int mg_version(void) { return 500; }   // 0.5.0: norms, modulation and residual around the block, GEMM epilogue
 
 const char* mg_last_error(void) { return g_err; }
 

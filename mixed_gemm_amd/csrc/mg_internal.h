@@ -103,4 +103,18 @@ int check_forward(const mg_plan* p, const void* X, int32_t dtype, int64_t M, con
 // returns code.
 int fail_msg(int code, const char* fmt, ...);
 
+// Host-side argument checks shared by the C entries; MG_OK or the error
+// (message set).
+bool aligned16(const void* p);
+int check_dtype(int32_t dtype);
+int check_plan(const mg_plan* p, bool need_w);
+int check_gemm_size(const mg_plan* p, int64_t M);
+int check_act(const mg_plan* p, const mg_act* a);
+
+#define MG_CHECK_PTR(p, name)                                                                          \
+    do {                                                                                               \
+        if ((p) == nullptr) return mg::fail_msg(MG_ERR_ARG, "%s: null pointer", name);                 \
+        if (!mg::aligned16(p)) return mg::fail_msg(MG_ERR_ALIGN, "%s: not 16-byte aligned", name);     \
+    } while (0)
+
 }  // namespace mg

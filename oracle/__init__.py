@@ -28,4 +28,4 @@ Every function in ``oracle.layer`` and ``oracle.mxfp4`` is pinned by a
 closed forms, exact rational arithmetic, special cases).  ``gelu_tanh`` is
 pinned against the closed form evaluated with ``math.tanh``.
 """
-from . import mxfp4, layer  # noqa: F401
+from . import block, mxfp4, layer  # noqa: F401

@@ -1,0 +1,544 @@
+"""The operators around the block (norm + modulation, gated residual + norm,
+norm + quantize, the dual GEMM's epilogue) against the float64 oracle.
+
+Bounds.  u = 2^-24.  A sum of K terms formed with at most D additions in a row
+is off by at most D u sum|x|, so the mean by D u A (A = mean|x|), the variance
+by a relative (D + 6) u plus (D u A)^2, and each further operation adds one u;
+`norm_bound` adds these up per element.  An output rounded to bf16 may be
+another 2^-8 of itself away.  D follows from the kernel's layout: 8 V values
+per thread, 6 steps in the wave, W waves.
+"""
+import numpy as np
+import pytest
+import torch
+
+import mixed_gemm_amd as mg
+import synth
+from oracle import block
+from tests.gpu_util import dev, host
+
+pytestmark = pytest.mark.gpu
+
+U = 2.0 ** -24
+TYPES = {"f32": torch.float32, "bf16": torch.bfloat16}
+
+
+def _depth(K):
+    nw = -(-K // 512)
+    V = -(-nw // 8)
+    V = V if V <= 4 else 8
+    return 8 * V + 6 + -(-nw // V)
+
+
+def f64(t):
+    return None if t is None else t.detach().double().cpu().numpy()
+
+
+def norm_bound(x, n, a, c, K, kind, eps):
+    """Absolute error of a f32 evaluation of n a + c (n the norm of x in f64, a
+    and c the folded weights, c already in absolute values)."""
+    D = _depth(K)
+    A = np.abs(x).mean(axis=1, keepdims=True)
+    mean = x.mean(axis=1, keepdims=True) if kind == "layer" else 0.0
+    rstd = 1 / np.sqrt(((x - mean) ** 2).mean(axis=1, keepdims=True) + eps)
+    off = D * U * A * rstd if kind == "layer" else 0.0
+    dn = off + np.abs(n) * (U * (D / 2 + 12) + off ** 2)
+    return np.abs(a) * dn + 6 * U * (np.abs(n * a) + c) + 1e-37
+
+
+def assert_close(got, ref, bound, out, what):
+    bound = np.asarray(bound) + (2.0 ** -8 * (np.abs(ref) + bound) if out == "bf16" else 0.0)
+    bad = ~(np.abs(got - ref) <= bound)
+    assert not bad.any(), f"{what}: {int(bad.sum())} of {bad.size} off, worst {np.max(np.abs(got - ref) / bound)} x the bound"
+
+
+def rows(rng, M, K, dtype, ld=0, mean=0.3, fill=float("nan")):
+    """[M][K] view of heavy-tailed rows `K + ld` apart whose gaps hold `fill`, and the base."""
+    x = rng.standard_normal((M, K)) + mean * rng.standard_normal(K)
+    x[:, rng.permutation(K)[: max(1, K // 50)]] *= 25.0
+    base = torch.full((M, K + ld), fill, dtype=TYPES[dtype], device="cuda")
+    base[:, :K] = torch.from_numpy(x).to("cuda").to(TYPES[dtype])
+    return base[:, :K], base
+
+
+def out_rows(M, K, dtype, ld):
+    """An output [M][K] with guard elements around and between its rows."""
+    base = torch.full((M * (K + ld) + 32,), 776.0, dtype=TYPES[dtype], device="cuda")
+    return base[16:16 + M * (K + ld)].view(M, K + ld)[:, :K], base
+
+
+def assert_guards(view, base, M, K, ld):
+    full = host(base.float())
+    inner = np.zeros(full.size, bool)
+    inner[16:16 + M * (K + ld)] = (np.arange(M * (K + ld)) % (K + ld)) < K
+    assert (full[~inner] == 776.0).all(), "written outside the rows"
+
+
+def modulation(rng, R, K, dtype, ld=0):
+    e = torch.from_numpy(0.3 * rng.standard_normal((R, 3 * K + ld))).to("cuda").to(TYPES[dtype])
+    return e[:, :K], e[:, K:2 * K], e[:, 2 * K:3 * K]
+
+
+def vec(rng, K, dtype, at=0.0):
+    return torch.from_numpy(at + 0.2 * rng.standard_normal(K)).to("cuda").to(TYPES[dtype])
+
+
+NORM_CASES = [
+    # M, K, x, out, kind, affine, modulation, its type, ld
+    (1, 1, "f32", "f32", "layer", None, None, "f32", 0),
+    (3, 7, "bf16", "f32", "rms", "bf16", "token", "bf16", 0),
+    (2, 8, "bf16", "bf16", "layer", "f32", "sample", "f32", 8),
+    (300, 31, "f32", "bf16", "layer", None, "token", "f32", 1),
+    (64, 512, "bf16", "f32", "layer", "bf16", "sample", "bf16", 0),
+    (7, 513, "bf16", "f32", "rms", None, "sample", "f32", 3),
+    (33, 1537, "bf16", "bf16", "rms", "bf16", "token", "bf16", 9),
+    (9, 5120, "f32", "f32", "layer", None, "sample", "f32", 0),
+    (530, 5120, "f32", "bf16", "layer", None, "token", "f32", 0),
+    (3, 5119, "f32", "f32", "layer", "f32", "sample", "bf16", 0),
+    (5, 13824, "bf16", "f32", "layer", "f32", "token", "f32", 8),
+    (4, 13817, "f32", "f32", "rms", "bf16", "sample", "f32", 1),
+    (2, 40001, "bf16", "f32", "layer", "bf16", "sample", "f32", 0),
+    (2, 65536, "f32", "f32", "layer", None, "sample", "f32", 0),
+]
+
+
+def _where(rng, mod, M, R):
+    if mod == "token":
+        idx = rng.integers(-1, R + 1, M).astype(np.int32)        # -1 and R are padding
+        return dict(index=torch.from_numpy(idx).cuda()), block.rows_of(M, R, idx)
+    g = -(-M // R)
+    return dict(group=g), block.rows_of(M, R, group=g)
+
+
+@pytest.mark.parametrize("M,K,xt,ht,kind,affine,mod,mt,ld", NORM_CASES)
+def test_norm_mod(M, K, xt, ht, kind, affine, mod, mt, ld):
+    rng = np.random.default_rng(M * 1000 + K)
+    X, _ = rows(rng, M, K, xt, ld)
+    w, b = (vec(rng, K, affine, 1.0), vec(rng, K, affine)) if affine else (None, None)
+    norm = mg.Norm(kind, w, b, 1e-6)
+    m, i, sc, sh = None, np.zeros(M, int), None, None
+    if mod:
+        R = 3
+        sc, sh, _ = modulation(rng, R, K, mt, ld)
+        where, i = _where(rng, mod, M, R)
+        m = mg.Mod(scale=sc, shift=sh, **where)
+    H, base = out_rows(M, K, ht, ld)
+    mg.mg_norm_mod(norm, m, X, H)
+    torch.cuda.synchronize()
+    x = f64(X)
+    n0 = block.norm(x, kind)
+    ref = block.modulate(block.norm(x, kind, f64(w), f64(b)), i, f64(sc), f64(sh))
+    k = np.maximum(i, 0)
+    s1 = 1.0 + (f64(sc)[k] if sc is not None else 0.0)
+    a = (1.0 if w is None else f64(w)) * s1
+    c = np.abs((0.0 if b is None else f64(b)) * s1) + (np.abs(f64(sh)[k]) if sh is not None else 0.0)
+    bound = norm_bound(x, n0, a, c, K, kind, 1e-6)
+    assert_close(f64(H), ref, bound, ht, "H")
+    assert (f64(H)[i < 0] == 0).all()
+    assert_guards(H, base, M, K, ld)
+
+
+def test_norm_mod_only_scale_or_shift_and_in_place():
+    rng = np.random.default_rng(5)
+    X, _ = rows(rng, 40, 96, "f32")
+    sc, sh, _ = modulation(rng, 1, 96, "f32")
+    x = f64(X)
+    for kw in (dict(scale=sc), dict(shift=sh)):
+        H = X.clone()
+        mg.mg_norm_mod(mg.Norm(), mg.Mod(**kw), H, H)
+        ref = block.modulate(block.norm(x), np.zeros(40, int), f64(kw.get("scale")), f64(kw.get("shift")))
+        a = 1.0 + (f64(sc)[0] if "scale" in kw else 0.0)
+        c = np.abs(f64(sh)[0]) if "shift" in kw else 0.0
+        assert_close(f64(H), ref, norm_bound(x, block.norm(x), a, c, 96, "layer", 1e-6), "f32", str(list(kw)))
+
+
+@pytest.mark.parametrize("K", [96, 5120, 5121])
+def test_norm_of_rows_far_from_zero(K):
+    """Rows whose mean is 4096 times their spread: a sum of squares would lose the variance."""
+    rng = np.random.default_rng(K)
+    X = torch.from_numpy(4096.0 + rng.standard_normal((5, K))).float().cuda()
+    H = torch.empty_like(X)
+    mg.mg_norm_mod(mg.Norm(), None, X, H)
+    x = f64(X)
+    n = block.norm(x)
+    assert_close(f64(H), n, norm_bound(x, n, 1.0, 0.0, K, "layer", 1e-6), "f32", "H")
+    assert norm_bound(x, n, 1.0, 0.0, K, "layer", 1e-6).max() < 0.05
+
+
+def test_constant_zero_and_extreme_rows():
+    K = 200
+    X = torch.zeros(5, K, device="cuda")
+    X[1] = 3.0
+    X[2] = torch.linspace(-1e-20, 1e-20, K)
+    X[3] = torch.linspace(-1e15, 1e15, K)
+    X[4, 7] = 1.0
+    H = torch.empty_like(X)
+    mg.mg_norm_mod(mg.Norm("layer"), None, X, H)
+    x = f64(X)
+    n = block.norm(x)
+    assert_close(f64(H), n, norm_bound(x, n, 1.0, 0.0, K, "layer", 1e-6), "f32", "H")
+    assert (f64(H)[0] == 0).all()
+
+
+def test_nan_and_infinity_stay_in_their_row_and_out_of_padding():
+    K, M = 600, 6
+    rng = np.random.default_rng(3)
+    X, _ = rows(rng, M, K, "f32")
+    Y, _ = rows(rng, M, K, "bf16")
+    X[1, 599] = float("nan")
+    X[3, 0] = float("inf")
+    X[4, 5] = float("nan")                     # padding
+    Y[5, 7] = float("inf")                     # padding
+    sc, sh, ga = modulation(rng, 2, K, "f32")
+    idx = torch.tensor([0, 1, 0, 1, -1, 2], dtype=torch.int32, device="cuda")
+    m = mg.Mod(scale=sc, shift=sh, gate=ga, index=idx)
+    H = torch.empty(M, K, device="cuda")
+    mg.mg_norm_mod(mg.Norm(), m, X, H)
+    h = f64(H)
+    assert np.isnan(h[1]).all() and not np.isfinite(h[3]).any()
+    assert np.isfinite(h[[0, 2]]).all() and (h[[4, 5]] == 0).all()
+    O = torch.empty_like(X)
+    mg.mg_residual_norm(X, Y, O, m, None, mg.Norm(), m, H)
+    o, h = f64(O), f64(H)
+    assert np.array_equal(o[4:], f64(X)[4:], equal_nan=True) and (h[4:] == 0).all()
+    assert np.isnan(h[1]).all() and np.isfinite(h[[0, 2]]).all()
+
+
+RES_CASES = [
+    # M, K, x, y, out, post, norm, modulation, its type, ld
+    (1, 1, "f32", "f32", "f32", False, None, "sample", "f32", 0),
+    (17, 5120, "bf16", "bf16", "bf16", False, "layer", "sample", "bf16", 0),
+    (70, 5120, "f32", "bf16", "bf16", False, "layer", "token", "f32", 0),
+    (29, 2049, "bf16", "bf16", "bf16", True, "rms", "token", "f32", 3),
+    (5, 13824, "f32", "f32", "f32", True, "layer", "sample", "bf16", 8),
+    (300, 77, "bf16", "f32", "f32", True, None, "token", "bf16", 1),
+    (3, 30011, "f32", "bf16", "f32", False, "rms", "sample", "f32", 0),
+    (2, 65536, "bf16", "bf16", "f32", True, "layer", "sample", "f32", 0),
+]
+
+
+@pytest.mark.parametrize("M,K,xt,yt,ht,post,kind,mod,mt,ld", RES_CASES)
+def test_residual_norm(M, K, xt, yt, ht, post, kind, mod, mt, ld):
+    rng = np.random.default_rng(M * 77 + K)
+    X, _ = rows(rng, M, K, xt, ld)
+    Y, _ = rows(rng, M, K, yt, ld)
+    sc, sh, ga = modulation(rng, 3, K, mt, ld)
+    where, i = _where(rng, mod, M, 3)
+    pw = vec(rng, K, "bf16", 1.0) if post else None
+    O, obase = out_rows(M, K, xt, ld)
+    H, hbase = out_rows(M, K, ht, ld) if kind else (None, None)
+    mg.mg_residual_norm(X, Y, O, mg.Mod(gate=ga, **where), mg.Norm("rms", pw) if post else None,
+                        mg.Norm(kind) if kind else None, mg.Mod(scale=sc, shift=sh, **where) if kind else None, H)
+    torch.cuda.synchronize()
+    x, y, k = f64(X), f64(Y), np.maximum(i, 0)
+    g = f64(ga)[k]
+    p = block.norm(y, "rms", f64(pw)) if post else y
+    o = block.gated(x, p, i, f64(ga))
+    dp = norm_bound(y, block.norm(y, "rms"), f64(pw), 0.0, K, "rms", 1e-6) if post else 0.0
+    do = np.where((i < 0)[:, None], 0.0, np.abs(g) * dp + 2 * U * (np.abs(x) + np.abs(g * p)))
+    assert_close(f64(O), o, do + 1e-37, xt, "O")
+    pad = i < 0
+    assert np.array_equal(f64(O)[pad], x[pad])
+    assert_guards(O, obase, M, K, ld)
+    if kind:
+        n = block.norm(o, kind)
+        ref = block.modulate(n, i, f64(sc), f64(sh))
+        a = 1.0 + f64(sc)[k]
+        mean = o.mean(axis=1, keepdims=True) if kind == "layer" else 0.0
+        rstd = 1 / np.sqrt(((o - mean) ** 2).mean(axis=1, keepdims=True) + 1e-6)
+        # the sum's own error passes through the norm: its own element's, and the mean's and spread's
+        thru = np.abs(a) * rstd * (do + do.mean(axis=1, keepdims=True) + np.abs(n) * np.sqrt((do ** 2).mean(axis=1, keepdims=True)))
+        bound = norm_bound(o, n, a, np.abs(f64(sh)[k]), K, kind, 1e-6) + thru
+        assert_close(f64(H), ref, bound, ht, "H")
+        assert (f64(H)[pad] == 0).all()
+        assert_guards(H, hbase, M, K, ld)
+
+
+def test_residual_in_place_and_plain_sum():
+    rng = np.random.default_rng(8)
+    X, _ = rows(rng, 50, 640, "bf16")
+    Y, _ = rows(rng, 50, 640, "bf16")
+    O, H = torch.empty_like(X), torch.empty_like(Y)
+    mg.mg_residual_norm(X, Y, O, None, None, mg.Norm(), None, H)
+    x, y = X.clone(), Y.clone()
+    mg.mg_residual_norm(x, y, x, None, None, mg.Norm(), None, y)
+    assert torch.equal(x, O) and torch.equal(y, H)
+    assert torch.equal(O, (X.float() + Y.float()).bfloat16())
+
+
+QUANT_CASES = [
+    # M, K, k, x, kind, affine, modulation, its type, ld
+    (1, 5120, 64, "bf16", "layer", None, "sample", "f32", 0),
+    (17, 32, 0, "f32", "rms", "bf16", "sample", "f32", 1),
+    (33, 352, 5, "bf16", "layer", "f32", "token", "bf16", 3),
+    (300, 1568, 40, "f32", "layer", None, "token", "f32", 0),
+    (515, 5120, 64, "f32", "layer", None, "sample", "f32", 0),
+    (70, 13824, 128, "bf16", "rms", "bf16", "sample", "bf16", 8),
+    (9, 16416, 300, "f32", "layer", None, "sample", "f32", 0),
+    (3, 65536, 17, "bf16", "layer", None, "token", "f32", 0),
+    (40, 544, 544, "bf16", "layer", None, "sample", "f32", 0),
+]
+
+
+def _quant_plan(rng, K, N, k, H):
+    W = dev(synth.weights(N, K, sigma=0.02, clip=0.6, seed=K + k, bf16=True))
+    act_max = H.abs().amax(0).float().clamp(min=1e-3) if H.shape[0] else torch.ones(K, device="cuda")
+    return mg.plan(act_max.contiguous(), W, 0.6, k)
+
+
+@pytest.mark.parametrize("M,K,k,xt,kind,affine,mod,mt,ld", QUANT_CASES)
+def test_norm_quantize_is_norm_then_quantize(M, K, k, xt, kind, affine, mod, mt, ld):
+    """Every byte, pads included, of mg_norm_mod into bf16 followed by mg_quantize_act."""
+    rng = np.random.default_rng(M + K)
+    X, _ = rows(rng, M, K, xt, ld)
+    w, b = (vec(rng, K, affine, 1.0), vec(rng, K, affine)) if affine else (None, None)
+    sc, sh, _ = modulation(rng, 3, K, mt, ld)
+    where, _ = _where(rng, mod, M, 3)
+    norm, m = mg.Norm(kind, w, b), mg.Mod(scale=sc, shift=sh, **where)
+    H = torch.empty(M, K, dtype=torch.bfloat16, device="cuda")
+    mg.mg_norm_mod(norm, m, X, H)
+    p = _quant_plan(rng, K, 32, k, H)
+    a, f = mg.Act.empty(p.desc, M), mg.Act.empty(p.desc, M)
+    for t in (a.Aq, a.As, a.XO, f.Aq, f.As, f.XO):
+        t.fill_(0xA5)
+    mg.mg_quantize_act(p, H, a)
+    mg.mg_norm_quantize_act(p, norm, m, X, f)
+    torch.cuda.synchronize()
+    for n in ("Aq", "As", "XO"):
+        x, y = host(getattr(a, n)), host(getattr(f, n))
+        assert np.array_equal(x, y), f"{n}: {int((x != y).sum())} of {x.size} bytes differ"
+
+
+def test_norm_quantize_with_scales_out_of_the_fast_range():
+    """Smoothing scales far from 1 and rows of tiny values: the exact division's codes."""
+    rng = np.random.default_rng(12)
+    M, K, k = 40, 1024, 24
+    X, _ = rows(rng, M, K, "f32")
+    X[7] *= 1e-30
+    p = _quant_plan(rng, K, 32, k, X.bfloat16())
+    s = torch.from_numpy(np.exp2(rng.uniform(-30, 30, K)).astype(np.float32)).cuda()
+    s[:512] = torch.from_numpy(np.exp2(rng.uniform(-3, 3, 512)).astype(np.float32)).cuda()
+    p.s.copy_(s)
+    p.rcp.copy_((1.0 / s.double()).float())
+    w = torch.from_numpy(np.exp2(rng.uniform(-90, 0, K)).astype(np.float32)).cuda()
+    norm, m = mg.Norm("layer", w), None
+    H = torch.empty(M, K, dtype=torch.bfloat16, device="cuda")
+    mg.mg_norm_mod(norm, m, X, H)
+    a, f = mg.Act.empty(p.desc, M), mg.Act.empty(p.desc, M)
+    mg.mg_quantize_act(p, H, a)
+    mg.mg_norm_quantize_act(p, norm, m, X, f)
+    for n in ("Aq", "As", "XO"):
+        assert np.array_equal(host(getattr(a, n)), host(getattr(f, n))), n
+
+
+# ------------------------------------------------------------------ epilogue
+
+def decoded(p, a, M):
+    """The fp32 sums' float64 value and the sum of their terms' magnitudes, from
+    the kernel's own operands (exact decode)."""
+    from oracle import mxfp4
+    from tests.gpu_util import aq_rows, outlier_cols, scale_rows
+    d = p.desc
+    A = mxfp4.decode_rows(aq_rows(a.Aq, M, d.K), scale_rows(a.As, M, d.K)).astype(np.float64)
+    W = mxfp4.decode_rows(aq_rows(p.Wq, d.N, d.K), scale_rows(p.Ws, d.N, d.K)).astype(np.float64)
+    v, t = A @ W.T, np.abs(A) @ np.abs(W).T
+    if d.k:
+        from tests.gpu_util import bf16_to_f64
+        x, w = bf16_to_f64(outlier_cols(a.XO, M, d.k)), bf16_to_f64(outlier_cols(p.WO, d.N, d.k))
+        v, t = v + x @ w.T, t + np.abs(x) @ np.abs(w).T
+    return v, t
+
+
+EP_CASES = [
+    # M, K, N, k, y, bias, act, gate, residual, modulation, its type
+    (1, 32, 32, 0, "f32", None, "none", False, None, "sample", "f32"),
+    (1, 5120, 1024, 64, "bf16", "bf16", "gelu", False, None, "sample", "f32"),
+    (17, 1568, 544, 40, "f32", "f32", "none", True, "f32", "sample", "f32"),
+    (31, 13824, 96, 128, "bf16", "bf16", "none", True, "bf16", "token", "bf16"),
+    (32, 512, 64, 5, "f32", "bf16", "silu", True, "bf16", "token", "f32"),
+    (33, 544, 1056, 544, "f32", "bf16", "gelu", False, None, "sample", "f32"),
+    (65, 5120, 160, 0, "bf16", None, "none", True, "f32", "sample", "bf16"),
+    (130, 2080, 320, 33, "f32", "f32", "gelu", True, "f32", "token", "f32"),
+    (300, 1056, 1312, 64, "bf16", "bf16", "silu", True, "bf16", "sample", "f32"),
+    (777, 1568, 1056, 40, "f32", "bf16", "none", True, "f32", "token", "f32"),
+    (1100, 640, 288, 16, "f32", None, "gelu", False, "bf16", "sample", "f32"),
+]
+
+
+@pytest.mark.parametrize("M,K,N,k,yt,bias,act,gate,res,mod,mt", EP_CASES)
+def test_gemm_epilogue(M, K, N, k, yt, bias, act, gate, res, mod, mt):
+    rng = np.random.default_rng(M + 3 * N + K)
+    X, _ = rows(rng, M, K, "bf16")
+    p = _quant_plan(rng, K, N, k, X)
+    a = mg.Act.empty(p.desc, M)
+    mg.mg_quantize_act(p, X, a)
+    b = vec(rng, N, bias) if bias else None
+    ga = modulation(rng, 3, N, mt, 8)[2] if gate else None
+    where, i = _where(rng, mod, M, 3)
+    g = mg.Mod(gate=ga, rows=3, **where) if gate or mod == "token" else None
+    R = rows(rng, M, N, res, 16)[0] if res else None
+    Y = torch.full((M + 1, N), float("nan"), dtype=TYPES[yt], device="cuda")
+    Y[M] = 776.0
+    mg.mg_dual_gemm_ep(p, a, mg.Epilogue(b, act, g, R), Y[:M])
+    Y2 = torch.full((M, N), float("nan"), dtype=TYPES[yt], device="cuda")
+    mg.mg_forward_ep(p, X, a, mg.Epilogue(b, act, g, R), Y2)
+    torch.cuda.synchronize()
+    v, t = decoded(p, a, M)
+    ref = block.epilogue(v, i if g is not None else np.zeros(M, int), f64(b), act, f64(ga), f64(R))
+    # K + k products summed in any order, then bias; GELU / SiLU: slope at most 1.13, their own
+    # evaluation off by (12 + 4 |exponent|) u of the result
+    dv = (K + k + 2) * U * t + U * (np.abs(v) + (0 if b is None else np.abs(f64(b))))
+    z = v + (0 if b is None else f64(b))
+    av = np.abs(block.activation(z, act))
+    if act != "none":
+        e = np.abs(z) * 1.4427 if act == "silu" else np.abs(2.3022 * z + 0.10295 * z ** 3)
+        dv = 1.13 * dv + av * (12 + 4 * e) * U + 1e-37
+    gg = 1.0 if ga is None else np.abs(f64(ga)[np.maximum(i, 0)])
+    live = (i >= 0)[:, None] if g is not None else True
+    dy = np.where(live, gg * dv + 3 * U * gg * av, 0.0) + U * np.abs(ref) + 1e-37
+    assert_close(f64(Y[:M]), ref, dy, yt, "Y")
+    assert (f64(Y[M]) == 776.0).all()
+    assert torch.equal(Y[:M], Y2), "forward_ep is quantize + gemm_ep"
+    for _ in range(3):
+        Y2.fill_(float("nan"))
+        mg.mg_dual_gemm_ep(p, a, mg.Epilogue(b, act, g, R), Y2)
+        assert torch.equal(Y[:M], Y2), "the same call gives the same bits"
+
+
+def test_epilogue_in_place_on_the_residual():
+    rng = np.random.default_rng(4)
+    for M, yt in ((9, "bf16"), (300, "f32"), (300, "bf16")):
+        X, _ = rows(rng, M, 512, "bf16")
+        p = _quant_plan(rng, 512, 320, 8, X)
+        a = mg.Act.empty(p.desc, M)
+        R, _ = rows(rng, M, 320, yt)
+        Y = torch.empty_like(R)
+        mg.mg_forward_ep(p, X, a, mg.Epilogue(residual=R), Y)
+        Z = R.clone()
+        mg.mg_forward_ep(p, X, a, mg.Epilogue(residual=Z), Z)
+        assert torch.equal(Y, Z), (M, yt)
+
+
+def test_no_epilogue_is_the_dual_gemm():
+    rng = np.random.default_rng(6)
+    X, _ = rows(rng, 2100, 1056, "bf16")
+    p = _quant_plan(rng, 1056, 1312, 20, X)
+    a = mg.Act.empty(p.desc, 2100)
+    mg.mg_quantize_act(p, X, a)
+    for dt in (torch.float32, torch.bfloat16):
+        Y, Z = (torch.empty(2100, 1312, dtype=dt, device="cuda") for _ in range(2))
+        mg.mg_dual_gemm(p, a, Y)
+        mg.mg_dual_gemm_ep(p, a, None, Z)
+        v, t = decoded(p, a, 2100)
+        assert_close(f64(Z), v, (1056 + 20) * U * t + 1e-37, "f32" if dt == torch.float32 else "bf16", "Y")
+
+
+def test_zero_rows_launch_nothing():
+    p = _quant_plan(np.random.default_rng(0), 64, 32, 4, torch.ones(1, 64, device="cuda"))
+    X = torch.empty(0, 64, dtype=torch.bfloat16, device="cuda")
+    a = mg.Act.empty(p.desc, 0)
+    mg.mg_norm_mod(mg.Norm(), None, X, X)
+    mg.mg_residual_norm(X, X, X)
+    mg.mg_norm_quantize_act(p, mg.Norm(), None, X, a)
+    mg.mg_forward_ep(p, X, a, None, torch.empty(0, 32, device="cuda"))
+    torch.cuda.synchronize()
+
+
+def test_on_another_stream():
+    rng = np.random.default_rng(9)
+    X, _ = rows(rng, 64, 512, "bf16")
+    p = _quant_plan(rng, 512, 64, 8, X)
+    a = mg.Act.empty(p.desc, 64)
+    Y, Z, H, H2 = (torch.empty(64, n, device="cuda") for n in (64, 64, 512, 512))
+    mg.mg_norm_mod(mg.Norm(), None, X, H)
+    mg.mg_forward_ep(p, X, a, mg.Epilogue(act="gelu"), Y)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    mg.mg_norm_mod(mg.Norm(), None, X, H2, stream=s)
+    mg.mg_forward_ep(p, X, a, mg.Epilogue(act="gelu"), Z, stream=s.cuda_stream)
+    s.synchronize()
+    assert torch.equal(H, H2) and torch.equal(Y, Z)
+
+
+def test_replayed_in_a_graph():
+    """norm + quantize -> GEMM with epilogue -> residual captured once and replayed on new inputs."""
+    rng = np.random.default_rng(10)
+    M, K, N = 70, 512, 512
+    X, _ = rows(rng, M, K, "bf16")
+    p = _quant_plan(rng, K, N, 8, X)
+    a = mg.Act.empty(p.desc, M)
+    sc, sh, ga = modulation(rng, 1, K, "f32")
+    b = vec(rng, N, "bf16")
+    Y, O = torch.empty(M, N, dtype=torch.bfloat16, device="cuda"), torch.empty_like(X)
+
+    def step():
+        mg.mg_norm_quantize_act(p, mg.Norm(), mg.Mod(scale=sc, shift=sh), X, a)
+        mg.mg_dual_gemm_ep(p, a, mg.Epilogue(b, "silu"), Y)
+        mg.mg_residual_norm(X, Y, O, mg.Mod(gate=ga))
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step()
+    for seed in range(5):
+        X.copy_(rows(np.random.default_rng(100 + seed), M, K, "bf16")[0])
+        O.fill_(float("nan"))
+        graph.replay()
+        torch.cuda.synchronize()
+        got = O.clone()
+        step()
+        torch.cuda.synchronize()
+        assert torch.equal(got, O), seed
+
+
+# ------------------------------------------------------------------ refusals
+
+def test_binding_refuses_what_does_not_fit():
+    X = torch.zeros(4, 64, device="cuda")
+    H = torch.zeros(4, 64, device="cuda")
+    V = lambda n: torch.zeros(n, device="cuda")  # noqa: E731
+    bad = pytest.raises((ValueError, mg.MGError))
+    with bad:
+        mg.mg_norm_mod(mg.Norm(weight=V(63)), None, X, H)
+    with bad:
+        mg.mg_norm_mod(mg.Norm(), mg.Mod(scale=torch.zeros(1, 32, device="cuda")), X, H)
+    with bad:
+        mg.mg_norm_mod(mg.Norm(), mg.Mod(scale=torch.zeros(1, 64, device="cuda"), index=V(3).int()), X, H)
+    with bad:
+        mg.mg_norm_mod(mg.Norm(), mg.Mod(scale=torch.zeros(1, 64, device="cuda"), group=2), X, H)   # 2 groups, 1 row
+    with bad:
+        mg.mg_norm_mod(mg.Norm(), None, X, H[:3])
+    with bad:
+        mg.mg_norm_mod(mg.Norm(), None, X.t(), X.t())                  # columns are not consecutive
+    with bad:
+        mg.mg_norm_mod(mg.Norm(), None, X, H.cpu())
+    with bad:
+        mg.mg_norm_mod(mg.Norm(), None, X, H.double())
+    with bad:
+        mg.mg_norm_mod(mg.Norm(), None, X, X[:1].expand(4, 64))        # overlapping rows
+    with bad:
+        mg.mg_residual_norm(X, H, H.bfloat16())                        # O of another type than X
+    with bad:
+        mg.mg_residual_norm(X, H, H, mod=mg.Mod(scale=torch.zeros(1, 64, device="cuda")))
+    with bad:
+        mg.Norm("batch")
+    with bad:
+        mg.Mod()
+    with bad:
+        mg.Epilogue(act="tanh")
+    with bad:
+        mg.Mod(scale=torch.zeros(2, 64, device="cuda"), shift=torch.zeros(3, 64, device="cuda"))
+    p = _quant_plan(np.random.default_rng(0), 64, 32, 4, X + 1)
+    a, Y = mg.Act.empty(p.desc, 4), torch.empty(4, 32, device="cuda")
+    with bad:
+        mg.mg_forward_ep(p, X, a, mg.Epilogue(bias=V(31)), Y)
+    with bad:
+        mg.mg_forward_ep(p, X, a, mg.Epilogue(residual=torch.zeros(5, 32, device="cuda")), Y)
+    with bad:
+        mg.mg_forward_ep(p, X, a, mg.Epilogue(residual=torch.zeros(4, 36, device="cuda")[:, :32]), Y)  # ldr % 8
+    with bad:
+        mg.mg_forward_ep(p, X, a, mg.Epilogue(bias=V(33)[1:]), Y)      # not 16-byte aligned
+    with bad:
+        mg.mg_norm_quantize_act(p, mg.Norm(), None, H[:3], a)
+    torch.cuda.synchronize()
