@@ -174,16 +174,18 @@ struct GemmArgs {
     EpArgs ep;          // bias, activation, gate and residual (EpOut)
 };
 
-// Output tag of the epilogue with bias, activation, gate and residual, writing
-// Y as T (float, or uint16_t for bf16).
+// Output tags of the epilogue with bias, activation, gate and residual
+// (gemm_epilogue.h): bias and activation only into bf16, or everything into T
+// (float, or uint16_t for bf16).
+struct EpBiasAct {};
 template <typename T>
-struct EpOut {};
+struct EpFull {};
 template <typename T>
-struct IsEp : std::false_type {};
+struct EpOf : std::false_type {};
+template <>
+struct EpOf<EpBiasAct> : std::true_type { using type = uint16_t; };
 template <typename T>
-struct IsEp<EpOut<T>> : std::true_type {
-    using type = T;
-};
+struct EpOf<EpFull<T>> : std::true_type { using type = T; };
 
 // Output tag of the epilogue that applies GELU to the bf16-rounded tile and
 // quantizes it as the next layer's activation, instead of writing Y.
@@ -222,6 +224,29 @@ __device__ __forceinline__ QuantArgs kernargs_per_tile() {
     KernargPtr p = (KernargPtr)__builtin_amdgcn_kernarg_segment_ptr();
     asm volatile("" : "+s"(p));
     return QuantArgs{p->s2, p->rcp2, p->pos2, p->Aq2, p->As2, p->XO2, p->M, p->N, p->k2};
+}
+
+// The epilogue's arguments, read the same way.
+__device__ __forceinline__ EpArgs ep_args_per_tile() {
+    KernargPtr p = (KernargPtr)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    EpArgs e;
+    e.bias = p->ep.bias;
+    e.residual = p->ep.residual;
+    e.mod.scale = nullptr;
+    e.mod.shift = nullptr;
+    e.mod.gate = p->ep.mod.gate;
+    e.mod.index = p->ep.mod.index;
+    e.mod.ld = p->ep.mod.ld;
+    e.mod.group = p->ep.mod.group;
+    e.mod.rows = p->ep.mod.rows;
+    e.mod.dtype = p->ep.mod.dtype;
+    e.ldr = p->ep.ldr;
+    e.bias_dtype = p->ep.bias_dtype;
+    e.residual_dtype = p->ep.residual_dtype;
+    e.act = p->ep.act;
+    e.gated = p->ep.gated;
+    return e;
 }
 
 // bytes of a buffer of `total` bytes from offset `from` on (0 past its end)
@@ -750,8 +775,21 @@ dual_gemm_tiled(GemmArgs g) {
             // every wave's staging reads are done (their data fed the stores
             // above) before the next copies reuse the slots
             __builtin_amdgcn_s_barrier();
-        } else if constexpr (IsEp<OutT>::value) {
-            ep_store<typename IsEp<OutT>::type, JB>(g.ep, g.Y, acc, o.m0 + wm * 128, o.n0 + wn * 32 * JB, M, N, l32, h);
+        } else if constexpr (EpOf<OutT>::value) {
+            using YT = typename EpOf<OutT>::type;
+            const EpArgs e = ep_args_per_tile();
+            uint32_t et = (uint32_t)tid;
+            asm volatile("" : "+v"(et));       // lane values formed per tile, as above
+            const uint64_t rowY = (uint64_t)N * sizeof(YT);
+            const int64_t rows_left = M - o.m0;
+            const __amdgpu_buffer_rsrc_t rY = make_rsrc(static_cast<uint8_t*>(g.Y) + o.m0 * (int64_t)rowY,
+                                                        (uint64_t)(rows_left < TBM ? rows_left : TBM) * rowY);
+            if constexpr (std::is_same_v<OutT, EpBiasAct>)
+                ep_bias_act_bf16<JB>(e, rY, acc, wm * 128, o.n0 + wn * 32 * JB, N, wbuf, et & 63u);
+            else
+                ep_full<YT, JB>(e, rY, acc, o.m0, wm * 128, o.n0 + wn * 32 * JB, M, N, wbuf, et & 63u);
+            // every wave's staging reads are done before the next copies reuse the slots
+            __builtin_amdgcn_s_barrier();
         } else {
             // fp32: four consecutive columns per register group -> 16-byte stores
             float* Yf = static_cast<float*>(g.Y);
@@ -894,7 +932,8 @@ hipError_t launch_dual_gemm_ep(const uint8_t* Aq, const uint8_t* As, const uint1
     if (M <= 0) return hipSuccess;
     GemmArgs a{Aq, As, XO, Wq, Ws, WO, Y, M, N, K, k, (int32_t)((M + TBM - 1) / TBM), (N + TBN - 1) / TBN,
                nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, 0, e};
-    return y_dtype == MG_BF16 ? launch_tiled<EpOut<uint16_t>>(a, st) : launch_tiled<EpOut<float>>(a, st);
+    if (y_dtype != MG_BF16) return launch_tiled<EpFull<float>>(a, st);
+    return e.residual || e.gated ? launch_tiled<EpFull<uint16_t>>(a, st) : launch_tiled<EpBiasAct>(a, st);
 }
 
 }  // namespace mg

@@ -13,6 +13,8 @@ int hip_status(hipError_t h, const char* where) {
     return h == hipSuccess ? MG_OK : fail_msg(MG_ERR_HIP, "%s: %s", where, hipGetErrorString(h));
 }
 
+constexpr int64_t kMaxEpRow = (1 << 20) - 256;   // 256 rows of 4-byte elements stay below 1 GiB
+
 size_t elem_size(int32_t dtype) { return dtype == MG_F32 ? 4 : 2; }
 
 // A pointer to elements of `dtype` (already checked): not null, aligned to them.
@@ -137,6 +139,10 @@ int check_gemm_ep(const mg_plan* p, const mg_act* a, int64_t M, const mg_epilogu
     if (int c = check_act(p, a)) return c;
     if (int c = check_gemm_size(p, M)) return c;
     MG_CHECK_PTR(Y, "Y");
+    // a tile's 256 rows of Y and of the residual are addressed with 32-bit offsets
+    if ((int64_t)p->d.N > kMaxEpRow || out->ldr > kMaxEpRow)
+        return fail_msg(MG_ERR_UNSUPPORTED, "N=%d or ldr=%lld exceeds %lld", p->d.N, (long long)out->ldr,
+                        (long long)kMaxEpRow);
     return MG_OK;
 }
 
