@@ -157,8 +157,8 @@ def _check(code: int) -> None:
 
 
 def _stream(stream) -> int:
-    if stream is None:
-        return torch.cuda.current_stream().cuda_stream
+    if stream is None:                    # torch's current stream, without building a Stream object
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, torch.cuda.Stream):
         return stream.cuda_stream
     return int(stream)
@@ -194,12 +194,14 @@ def _ptr(t: torch.Tensor | None) -> int | None:
     return t.data_ptr()
 
 
+_DTYPES = {torch.float32: MG_F32, torch.bfloat16: MG_BF16, torch.int16: MG_BF16, torch.uint16: MG_BF16}
+
+
 def _dtype(t: torch.Tensor) -> int:
-    if t.dtype == torch.float32:
-        return MG_F32
-    if t.dtype in (torch.bfloat16, torch.int16, torch.uint16):
-        return MG_BF16
-    raise ValueError(f"unsupported dtype {t.dtype}")
+    d = _DTYPES.get(t.dtype)
+    if d is None:
+        raise ValueError(f"unsupported dtype {t.dtype}")
+    return d
 
 
 # The C ABI receives bare pointers and cannot know buffer sizes, so the binding
@@ -313,8 +315,11 @@ class Plan:
         return p
 
     def c(self) -> mg_plan:
-        return mg_plan(self.desc, _ptr(self.s), _ptr(self.rcp), _ptr(self.O), _ptr(self.pos), _ptr(self.Wq),
-                       _ptr(self.Ws), _ptr(self.Wst), _ptr(self.WO))
+        t = (self.s, self.rcp, self.O, self.pos, self.Wq, self.Ws, self.Wst, self.WO)
+        for x in t:
+            if not (x.is_cuda and x.is_contiguous()):
+                _ptr(x)                    # raises, unless it is empty
+        return mg_plan(self.desc, *[x.data_ptr() or None for x in t])
 
     def tensors(self) -> dict:
         return dict(s=self.s, rcp=self.rcp, O=self.O, pos=self.pos, Wq=self.Wq, Ws=self.Ws, Wst=self.Wst,
@@ -511,19 +516,54 @@ def mg_pct_select(st: PctState, pass_: int, q: float, score: torch.Tensor | None
 
 # ----------------------------------------------------------------------------- around the block
 
+# These calls are short (a few tokens take microseconds), so their checks take
+# a direct route: messages are formed only where one fails, and the C structs
+# of a Norm, Mod and Epilogue are made once, with the object that holds their
+# tensors.
+
 def _ref(x):
     """The C struct of a Norm, Mod or Epilogue (None: a null pointer)."""
-    return None if x is None else ctypes.byref(x.c)
+    return None if x is None else x.ref
 
 
 def _rows(t: torch.Tensor, name: str, cols: int | None = None) -> tuple[int, int]:
     """Rows of consecutive elements at any distance: (rows, elements between rows)."""
-    M, K = _matrix(t, name, cols)
-    _need(t.is_cuda, f"{name}: device tensor expected")
-    _need(K <= 1 or t.stride(1) == 1, f"{name}: the elements of a row must be consecutive, got strides {t.stride()}")
-    ld = t.stride(0) if M > 1 else max(K, t.stride(0))
-    _need(ld >= K, f"{name}: rows must not overlap, got strides {t.stride()}")
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 2 or (cols is not None and shape[1] != cols):
+        _matrix(t, name, cols)                                         # raises
+    M, K = shape
+    ld = strides[0]
+    if M <= 1 and ld < K:
+        ld = K
+    if not t.is_cuda:
+        raise ValueError(f"{name}: device tensor expected")
+    if strides[1] != 1 and K > 1:
+        raise ValueError(f"{name}: the elements of a row must be consecutive, got strides {strides}")
+    if ld < K:
+        raise ValueError(f"{name}: rows must not overlap, got strides {strides}")
     return M, ld
+
+
+def _act_struct(desc, act: "Act", M: int | None = None) -> mg_act:
+    """The C struct of a workspace that fits the plan and M rows."""
+    m, ns, nso = act.M, 2 * -(-desc.K // 128), 2 * -(-desc.k // 32)    # K / 2 and 2 k bytes a row, 64 a pair of slices
+    g = -(-m // 32)
+    Aq, As, XO = act.Aq, act.As, act.XO
+    if (m != M and M is not None) or Aq.dtype != torch.uint8 or Aq.shape != (g, ns, 1024) \
+            or _nbytes(As) != -(-m // 256) * -(-desc.K // 512) * 4096 or _nbytes(XO) != g * nso * 1024:
+        _check_act(desc, act, M)
+    if not (Aq.is_cuda and Aq.is_contiguous() and As.is_contiguous() and XO.is_contiguous()):
+        return act.c()                                                 # raises
+    return mg_act(Aq.data_ptr() or None, As.data_ptr() or None, XO.data_ptr() or None)
+
+
+def _out(desc, Y: torch.Tensor, M: int) -> tuple:
+    """Address and type of an output [M][N]."""
+    if Y.shape != (M, desc.N) or Y.dtype not in _DTYPES:
+        _check_y(desc, Y, M)
+    if not (Y.is_cuda and Y.is_contiguous()):
+        _ptr(Y)                                                        # raises
+    return Y.data_ptr(), _DTYPES[Y.dtype]
 
 
 class Norm:
@@ -544,6 +584,7 @@ class Norm:
         self.weight, self.bias = weight, bias
         t = weight if weight is not None else bias
         self.c = mg_norm(_ptr(weight), _ptr(bias), MG_F32 if t is None else _dtype(t), NORMS[kind], float(eps))
+        self.ref = ctypes.pointer(self.c)
 
 
 class Mod:
@@ -576,19 +617,27 @@ class Mod:
         ptr = lambda t: None if t is None else t.data_ptr()  # noqa: E731
         self.c = mg_mod(ptr(scale), ptr(shift), ptr(gate), _ptr(index), (1 << 62) if group is None else int(group),
                         ld, rows, dtype)
+        self.ref = ctypes.pointer(self.c)
 
 
 def _check_norm(n: Norm | None, K: int, name: str) -> None:
-    if n is not None:
-        _need(isinstance(n, Norm), f"{name} must be a Norm")
-        _need(n.width in (None, K), f"{name} is for {n.width} channels, the rows have {K}")
+    if n is None:
+        return
+    if not isinstance(n, Norm):
+        raise ValueError(f"{name} must be a Norm")
+    if n.width is not None and n.width != K:
+        raise ValueError(f"{name} is for {n.width} channels, the rows have {K}")
 
 
 def _check_mod(m: Mod | None, M: int, K: int, name: str) -> None:
-    if m is not None:
-        _need(isinstance(m, Mod), f"{name} must be a Mod")
-        _need(m.width in (None, K), f"{name} is for {m.width} channels, the rows have {K}")
-        _need(m.tokens in (None, M), f"{name} has an index of {m.tokens} tokens, the input has {M} rows")
+    if m is None:
+        return
+    if not isinstance(m, Mod):
+        raise ValueError(f"{name} must be a Mod")
+    if m.width is not None and m.width != K:
+        raise ValueError(f"{name} is for {m.width} channels, the rows have {K}")
+    if m.tokens is not None and m.tokens != M:
+        raise ValueError(f"{name} has an index of {m.tokens} tokens, the input has {M} rows")
 
 
 class Epilogue:
@@ -604,14 +653,16 @@ class Epilogue:
         ldr = _rows(residual, "residual")[1] if residual is not None else 0
         self.bias, self.gate, self.residual = bias, gate, residual
         self.c = mg_epilogue(_ptr(bias), None if residual is None else residual.data_ptr(),
-                             None if gate is None else ctypes.pointer(gate.c), ldr,
-                             MG_F32 if bias is None else _dtype(bias),
+                             None if gate is None else gate.ref, ldr, MG_F32 if bias is None else _dtype(bias),
                              MG_F32 if residual is None else _dtype(residual), ACTS[act], 0)
+        self.ref = ctypes.pointer(self.c)
 
     def check(self, M: int, N: int) -> None:
-        _need(self.bias is None or self.bias.shape[0] == N, f"bias must have {N} elements")
+        if self.bias is not None and self.bias.shape[0] != N:
+            raise ValueError(f"bias must have {N} elements")
         _check_mod(self.gate, M, N, "gate")
-        _need(self.residual is None or tuple(self.residual.shape) == (M, N), f"residual must be [{M}][{N}]")
+        if self.residual is not None and self.residual.shape != (M, N):
+            raise ValueError(f"residual must be [{M}][{N}]")
 
 
 def mg_norm_mod(norm: Norm, mod: Mod | None, X: torch.Tensor, H: torch.Tensor, stream=None) -> None:
@@ -619,11 +670,14 @@ def mg_norm_mod(norm: Norm, mod: Mod | None, X: torch.Tensor, H: torch.Tensor, s
     M, ldx = _rows(X, "X")
     K = X.shape[1]
     Mh, ldh = _rows(H, "H", K)
-    _need(Mh == M, f"H must have {M} rows, got {Mh}")
+    if Mh != M:
+        raise ValueError(f"H must have {M} rows, got {Mh}")
     _check_norm(norm, K, "norm")
     _check_mod(mod, M, K, "mod")
-    _check(lib().mg_norm_mod(_ref(norm), _ref(mod), X.data_ptr(), _dtype(X), ldx, M, K, H.data_ptr(), _dtype(H), ldh,
-                             _stream(stream)))
+    code = lib().mg_norm_mod(_ref(norm), _ref(mod), X.data_ptr(), _dtype(X), ldx, M, K, H.data_ptr(), _dtype(H), ldh,
+                             _stream(stream))
+    if code:
+        _check(code)
 
 
 def mg_residual_norm(X: torch.Tensor, Y: torch.Tensor, O: torch.Tensor, gate: Mod | None = None,
@@ -635,57 +689,68 @@ def mg_residual_norm(X: torch.Tensor, Y: torch.Tensor, O: torch.Tensor, gate: Mo
     K = X.shape[1]
     My, ldy = _rows(Y, "Y", K)
     Mo, ldo = _rows(O, "O", K)
-    _need(My == M and Mo == M, f"Y and O must have {M} rows, got {My} and {Mo}")
-    _need(_dtype(O) == _dtype(X), "O must have X's type")
+    if My != M or Mo != M:
+        raise ValueError(f"Y and O must have {M} rows, got {My} and {Mo}")
+    _need(O.dtype == X.dtype, "O must have X's type")
     _need((norm is None) == (H is None), "H goes with norm")
     _need(norm is not None or mod is None, "mod goes with norm")
     ldh, h, h_dtype = 0, None, MG_BF16
     if H is not None:
         Mh, ldh = _rows(H, "H", K)
-        _need(Mh == M, f"H must have {M} rows, got {Mh}")
+        if Mh != M:
+            raise ValueError(f"H must have {M} rows, got {Mh}")
         h, h_dtype = H.data_ptr(), _dtype(H)
     _check_norm(post, K, "post")
     _check_norm(norm, K, "norm")
     _check_mod(gate, M, K, "gate")
     _check_mod(mod, M, K, "mod")
-    ptr = lambda x: None if x is None else ctypes.pointer(x.c)  # noqa: E731
     a = mg_residual(X.data_ptr(), Y.data_ptr(), O.data_ptr(), h, ldx, ldy, ldo, ldh, _dtype(X), _dtype(Y), h_dtype, 0,
-                    ptr(gate), ptr(post), ptr(norm), ptr(mod))
-    _check(lib().mg_residual_norm(ctypes.byref(a), M, K, _stream(stream)))
+                    _ref(gate), _ref(post), _ref(norm), _ref(mod))
+    code = lib().mg_residual_norm(ctypes.byref(a), M, K, _stream(stream))
+    if code:
+        _check(code)
 
 
 def mg_norm_quantize_act(plan: Plan, norm: Norm, mod: Mod | None, X: torch.Tensor, act: Act, stream=None) -> None:
     """mg_norm_mod into bf16, then mg_quantize_act, in one pass (the same bits)."""
-    M, ldx = _rows(X, "X", plan.desc.K)
-    _check_act(plan.desc, act, M)
-    _check_norm(norm, plan.desc.K, "norm")
-    _check_mod(mod, M, plan.desc.K, "mod")
-    p, a = plan.c(), act.c()
-    _check(lib().mg_norm_quantize_act(ctypes.byref(p), _ref(norm), _ref(mod), X.data_ptr(), _dtype(X), ldx, M,
-                                      ctypes.byref(a), _stream(stream)))
+    desc = plan.desc
+    M, ldx = _rows(X, "X", desc.K)
+    a = _act_struct(desc, act, M)
+    _check_norm(norm, desc.K, "norm")
+    _check_mod(mod, M, desc.K, "mod")
+    p = plan.c()
+    code = lib().mg_norm_quantize_act(ctypes.byref(p), _ref(norm), _ref(mod), X.data_ptr(), _dtype(X), ldx, M,
+                                      ctypes.byref(a), _stream(stream))
+    if code:
+        _check(code)
 
 
 def mg_dual_gemm_ep(plan: Plan, act: Act, ep: Epilogue | None, Y: torch.Tensor, stream=None) -> None:
     """mg_dual_gemm with bias, activation, gate and residual in its epilogue."""
-    _check_act(plan.desc, act)
-    _check_y(plan.desc, Y, act.M)
+    desc, M = plan.desc, act.M
+    a = _act_struct(desc, act)
+    y, y_dtype = _out(desc, Y, M)
     if ep is not None:
-        ep.check(act.M, plan.desc.N)
-    p, a = plan.c(), act.c()
-    _check(lib().mg_dual_gemm_ep(ctypes.byref(p), ctypes.byref(a), act.M, _ref(ep), _ptr(Y), _dtype(Y),
-                                 _stream(stream)))
+        ep.check(M, desc.N)
+    p = plan.c()
+    code = lib().mg_dual_gemm_ep(ctypes.byref(p), ctypes.byref(a), M, _ref(ep), y, y_dtype, _stream(stream))
+    if code:
+        _check(code)
 
 
 def mg_forward_ep(plan: Plan, X: torch.Tensor, act: Act, ep: Epilogue | None, Y: torch.Tensor, stream=None) -> None:
     """mg_quantize_act, then mg_dual_gemm_ep."""
-    M, _ = _matrix(X, "X", plan.desc.K)
-    _check_act(plan.desc, act, M)
-    _check_y(plan.desc, Y, M)
+    desc = plan.desc
+    M, _ = _matrix(X, "X", desc.K)
+    a = _act_struct(desc, act, M)
+    y, y_dtype = _out(desc, Y, M)
     if ep is not None:
-        ep.check(M, plan.desc.N)
-    p, a = plan.c(), act.c()
-    _check(lib().mg_forward_ep(ctypes.byref(p), _ptr(X), _dtype(X), M, ctypes.byref(a), _ref(ep), _ptr(Y), _dtype(Y),
-                               _stream(stream)))
+        ep.check(M, desc.N)
+    p = plan.c()
+    code = lib().mg_forward_ep(ctypes.byref(p), _ptr(X), _dtype(X), M, ctypes.byref(a), _ref(ep), y, y_dtype,
+                               _stream(stream))
+    if code:
+        _check(code)
 
 
 # ----------------------------------------------------------------------------- convenience
