@@ -46,7 +46,7 @@ __device__ __forceinline__ float ep_act(float v) {
 
 // f(integral_constant<int, act>)
 template <typename F>
-__device__ __forceinline__ void ep_by_act(int act, F&& f) {
+__host__ __device__ __forceinline__ void ep_by_act(int act, F&& f) {
     if (act == MG_ACT_GELU_TANH) f(std::integral_constant<int, MG_ACT_GELU_TANH>{});
     else if (act == MG_ACT_SILU) f(std::integral_constant<int, MG_ACT_SILU>{});
     else f(std::integral_constant<int, MG_ACT_NONE>{});
@@ -73,7 +73,19 @@ __device__ __forceinline__ void ep_load(__amdgpu_buffer_rsrc_t r, uint32_t off, 
     }
 }
 
-// 8 consecutive elements of type dtype from a 16-byte aligned place on.
+// 4 or 8 consecutive elements from a place aligned to them on.
+__device__ __forceinline__ void ep_load4(const void* p, int64_t at, bool f32, float (&v)[4]) {
+    if (f32) {
+        const ep_f32x4 a = *reinterpret_cast<const ep_f32x4*>(static_cast<const float*>(p) + at);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v[c] = a[c];
+    } else {
+        const ep_u32x2 w = *reinterpret_cast<const ep_u32x2*>(static_cast<const uint16_t*>(p) + at);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) v[c] = __uint_as_float(c & 1 ? w[c >> 1] & 0xFFFF0000u : w[c >> 1] << 16);
+    }
+}
+
 __device__ __forceinline__ void ep_load8(const void* p, int64_t at, bool f32, float (&v)[8]) {
     if (f32) {
         const ep_f32x4* x = reinterpret_cast<const ep_f32x4*>(static_cast<const float*>(p) + at);
@@ -89,7 +101,7 @@ __device__ __forceinline__ void ep_load8(const void* p, int64_t at, bool f32, fl
 
 // Bias and activation into bf16.  (m0, n0): the part's first row and column;
 // rY covers the tile's rows of Y from row m0 - mt0 on (byte range rows * 2 N).
-template <int JB, typename ACC>
+template <int ACT, int JB, typename ACC>
 __device__ __forceinline__ void ep_bias_act_bf16(const EpArgs& e, __amdgpu_buffer_rsrc_t rY, ACC& acc, uint32_t mt0,
                                                  int n0, int N, uint8_t* wbuf, uint32_t lane) {
     constexpr uint32_t CH = 4 * JB, RBY = 64 * JB;                // 16-byte chunks and bytes per staged row
@@ -104,49 +116,48 @@ __device__ __forceinline__ void ep_bias_act_bf16(const EpArgs& e, __amdgpu_buffe
             ep_load<4>(rB, (uint32_t)(n0 + 32 * j + 8 * q + 4 * (int)h) * (bf32 ? 4u : 2u), bf32, b[j][q]);
     const int gcol = n0 + (int)cl * 8;
     const uint32_t rowY = 2u * (uint32_t)N;
-    ep_by_act(e.act, [&](auto A) {
 #pragma unroll
-        for (int p = 0; p < 2; ++p) {
+    for (int p = 0; p < 2; ++p) {
 #pragma unroll
-            for (int ii = 0; ii < 2; ++ii) {
-                const int i = 2 * p + ii;
+        for (int ii = 0; ii < 2; ++ii) {
+            const int i = 2 * p + ii;
 #pragma unroll
-                for (int j = 0; j < JB; ++j) asm volatile("" : "+a"(acc[i][j]));    // read here, not earlier
-                const uint32_t r = (uint32_t)(32 * ii) + l32;
-                const uint32_t rb = r * RBY + h * 8, rs = r & (CH - 1);
+            for (int j = 0; j < JB; ++j) asm volatile("" : "+a"(acc[i][j]));    // read here, not earlier
+            const uint32_t r = (uint32_t)(32 * ii) + l32;
+            const uint32_t rb = r * RBY + h * 8, rs = r & (CH - 1);
 #pragma unroll
-                for (int j = 0; j < JB; ++j)
+            for (int j = 0; j < JB; ++j)
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        float v[4];
+                for (int q = 0; q < 4; ++q) {
+                    float v[4];
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) v[c] = ep_act<decltype(A)::value>(acc[i][j][4 * q + c] + b[j][q][c]);
-                        *reinterpret_cast<ep_u32x2*>(wbuf + rb + ((((uint32_t)(4 * j + q)) ^ rs) << 4)) =
-                            ep_u32x2{ep_pack(v[0], v[1]), ep_pack(v[2], v[3])};
-                    }
-            }
-#pragma unroll
-            for (int s0 = 0; s0 < (int)CH; s0 += 4) {
-                ep_u32x4 v[4];
-#pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    const uint32_t rr = (uint32_t)(64 / CH * (s0 + s)) + rl;
-                    v[s] = *reinterpret_cast<const ep_u32x4*>(wbuf + rr * RBY + ((cl ^ (rr & (CH - 1))) << 4));
+                    for (int c = 0; c < 4; ++c) v[c] = ep_act<ACT>(acc[i][j][4 * q + c] + b[j][q][c]);
+                    *reinterpret_cast<ep_u32x2*>(wbuf + rb + ((((uint32_t)(4 * j + q)) ^ rs) << 4)) =
+                        ep_u32x2{ep_pack(v[0], v[1]), ep_pack(v[2], v[3])};
                 }
-#pragma unroll
-                for (int s = 0; s < 4; ++s) {
-                    const uint32_t rr = (uint32_t)(64 / CH * (s0 + s)) + rl;
-                    const uint32_t off = gcol < N ? (mt0 + 64u * p + rr) * rowY + 2u * (uint32_t)gcol : kEpNowhere;
-                    __builtin_amdgcn_raw_buffer_store_b128(v[s], rY, off, 0, 2);
-                }
-            }
-            __builtin_amdgcn_sched_barrier(0);
         }
-    });
+#pragma unroll
+        for (int s0 = 0; s0 < (int)CH; s0 += 4) {
+            ep_u32x4 v[4];
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const uint32_t rr = (uint32_t)(64 / CH * (s0 + s)) + rl;
+                v[s] = *reinterpret_cast<const ep_u32x4*>(wbuf + rr * RBY + ((cl ^ (rr & (CH - 1))) << 4));
+            }
+#pragma unroll
+            for (int s = 0; s < 4; ++s) {
+                const uint32_t rr = (uint32_t)(64 / CH * (s0 + s)) + rl;
+                const uint32_t off = gcol < N ? (mt0 + 64u * p + rr) * rowY + 2u * (uint32_t)gcol : kEpNowhere;
+                __builtin_amdgcn_raw_buffer_store_b128(v[s], rY, off, 0, 2);
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    }
 }
 
-// Everything, into bf16 or f32 (YT uint16_t or float).
-template <typename YT, int JB, typename ACC>
+// Everything, into bf16 or f32 (YT uint16_t or float), with an f32 residual
+// (RF32) or a bf16 one or none.
+template <typename YT, int ACT, bool RF32, int JB, typename ACC>
 __device__ __forceinline__ void ep_full(const EpArgs& e, __amdgpu_buffer_rsrc_t rY, ACC& acc, int64_t tile_m0,
                                         uint32_t mt0, int n0, int64_t M, int N, uint8_t* wbuf, uint32_t lane) {
     constexpr bool YF = std::is_same_v<YT, float>;
@@ -155,7 +166,7 @@ __device__ __forceinline__ void ep_full(const EpArgs& e, __amdgpu_buffer_rsrc_t 
     const uint32_t l32 = lane & 31u, h = lane >> 5, rl = lane / LR, cl = lane & (LR - 1);
     const int gcol = n0 + (int)cl * 8;
     const bool col_ok = gcol < N;
-    const bool bf32 = e.bias_dtype == MG_F32, gf32 = e.mod.dtype == MG_F32, rf32 = e.residual_dtype == MG_F32;
+    const bool bf32 = e.bias_dtype == MG_F32, gf32 = e.mod.dtype == MG_F32;
     const int64_t left = M - tile_m0;
     const uint32_t nrow = (uint32_t)(left < 256 ? left : 256);
     float b[8] = {}, g[8] = {1, 1, 1, 1, 1, 1, 1, 1};
@@ -170,15 +181,15 @@ __device__ __forceinline__ void ep_full(const EpArgs& e, __amdgpu_buffer_rsrc_t 
     };
     if (one && e.mod.gate) ep_load<8>(gate_rsrc(i0), (uint32_t)gcol * gs, gf32, g);
     // the tile's rows of the residual; out of range (no residual, rows past M) reads 0
-    const uint32_t rs = rf32 ? 4u : 2u, rowR = (uint32_t)e.ldr * rs;
+    const uint32_t rs = RF32 ? 4u : 2u, rowR = (uint32_t)e.ldr * rs;
     const __amdgpu_buffer_rsrc_t rR = make_rsrc(static_cast<const uint8_t*>(e.residual) + tile_m0 * (int64_t)rowR,
                                                 e.residual ? (uint64_t)(nrow - 1u) * rowR + (uint64_t)N * rs : 0);
-    ep_u32x4 res[ST][2];               // the residual of each step, loaded one pass ahead
+    ep_u32x4 res[ST][RF32 ? 2 : 1];               // the residual of each step, loaded one pass ahead
     const uint32_t offR = col_ok ? (mt0 + rl) * rowR + (uint32_t)gcol * rs : kEpNowhere;
     auto load_res = [&](int p, int s) {
-        const uint32_t off = offR + (32u * p + RS * s) * rowR;      // kEpNowhere + 256 rows stays out of range
+        const uint32_t off = offR + (32u * p + RS * s) * rowR;      // kEpNowhere plus a tile stays out of range
         res[s][0] = __builtin_bit_cast(ep_u32x4, __builtin_amdgcn_raw_buffer_load_b128(rR, off, 0, 2));
-        if (rf32) res[s][1] = __builtin_bit_cast(ep_u32x4, __builtin_amdgcn_raw_buffer_load_b128(rR, off + 16u, 0, 2));
+        if constexpr (RF32) res[s][1] = __builtin_bit_cast(ep_u32x4, __builtin_amdgcn_raw_buffer_load_b128(rR, off + 16u, 0, 2));
     };
     if (e.residual) {
 #pragma unroll
@@ -213,17 +224,15 @@ __device__ __forceinline__ void ep_full(const EpArgs& e, __amdgpu_buffer_rsrc_t 
 #pragma unroll
                 for (int d = 0; d < 4; ++d) v[4 * c + d] = w[d] + b[4 * c + d];
             }
-            ep_by_act(e.act, [&](auto A) {
 #pragma unroll
-                for (int c = 0; c < 8; ++c) v[c] = ep_act<decltype(A)::value>(v[c]);
-            });
+            for (int c = 0; c < 8; ++c) v[c] = ep_act<ACT>(v[c]);
             float r[8] = {};
             if (e.residual) {
 #pragma unroll
                 for (int c = 0; c < 8; ++c) {
                     const ep_u32x4* x = res[s];
-                    r[c] = rf32 ? __uint_as_float(x[c >> 2][c & 3])
-                                : __uint_as_float(c & 1 ? x[0][c >> 1] & 0xFFFF0000u : x[0][c >> 1] << 16);
+                    if constexpr (RF32) r[c] = __uint_as_float(x[c >> 2][c & 3]);
+                    else r[c] = __uint_as_float(c & 1 ? x[0][c >> 1] & 0xFFFF0000u : x[0][c >> 1] << 16);
                 }
                 if (p < 3) load_res(p + 1, s);
             }

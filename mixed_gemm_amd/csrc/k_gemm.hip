@@ -177,15 +177,24 @@ struct GemmArgs {
 // Output tags of the epilogue with bias, activation, gate and residual
 // (gemm_epilogue.h): bias and activation only into bf16, or everything into T
 // (float, or uint16_t for bf16).
+template <int ACT>
 struct EpBiasAct {};
-template <typename T>
+template <typename T, int ACT, bool RF32>
 struct EpFull {};
 template <typename T>
 struct EpOf : std::false_type {};
-template <>
-struct EpOf<EpBiasAct> : std::true_type { using type = uint16_t; };
-template <typename T>
-struct EpOf<EpFull<T>> : std::true_type { using type = T; };
+template <int ACT>
+struct EpOf<EpBiasAct<ACT>> : std::true_type {
+    using type = uint16_t;
+    static constexpr bool full = false, rf32 = false;
+    static constexpr int act = ACT;
+};
+template <typename T, int ACT, bool RF32>
+struct EpOf<EpFull<T, ACT, RF32>> : std::true_type {
+    using type = T;
+    static constexpr bool full = true, rf32 = RF32;
+    static constexpr int act = ACT;
+};
 
 // Output tag of the epilogue that applies GELU to the bf16-rounded tile and
 // quantizes it as the next layer's activation, instead of writing Y.
@@ -784,10 +793,10 @@ dual_gemm_tiled(GemmArgs g) {
             const int64_t rows_left = M - o.m0;
             const __amdgpu_buffer_rsrc_t rY = make_rsrc(static_cast<uint8_t*>(g.Y) + o.m0 * (int64_t)rowY,
                                                         (uint64_t)(rows_left < TBM ? rows_left : TBM) * rowY);
-            if constexpr (std::is_same_v<OutT, EpBiasAct>)
-                ep_bias_act_bf16<JB>(e, rY, acc, wm * 128, o.n0 + wn * 32 * JB, N, wbuf, et & 63u);
+            if constexpr (!EpOf<OutT>::full)
+                ep_bias_act_bf16<EpOf<OutT>::act, JB>(e, rY, acc, wm * 128, o.n0 + wn * 32 * JB, N, wbuf, et & 63u);
             else
-                ep_full<YT, JB>(e, rY, acc, o.m0, wm * 128, o.n0 + wn * 32 * JB, M, N, wbuf, et & 63u);
+                ep_full<YT, EpOf<OutT>::act, EpOf<OutT>::rf32, JB>(e, rY, acc, o.m0, wm * 128, o.n0 + wn * 32 * JB, M, N, wbuf, et & 63u);
             // every wave's staging reads are done before the next copies reuse the slots
             __builtin_amdgcn_s_barrier();
         } else {
@@ -932,8 +941,18 @@ hipError_t launch_dual_gemm_ep(const uint8_t* Aq, const uint8_t* As, const uint1
     if (M <= 0) return hipSuccess;
     GemmArgs a{Aq, As, XO, Wq, Ws, WO, Y, M, N, K, k, (int32_t)((M + TBM - 1) / TBM), (N + TBN - 1) / TBN,
                nullptr, nullptr, nullptr, nullptr, nullptr, nullptr, 0, e};
-    if (y_dtype != MG_BF16) return launch_tiled<EpFull<float>>(a, st);
-    return e.residual || e.gated ? launch_tiled<EpFull<uint16_t>>(a, st) : launch_tiled<EpBiasAct>(a, st);
+    hipError_t r = hipErrorInvalidValue;
+    ep_by_act(e.act, [&](auto A) {
+        constexpr int ACT = decltype(A)::value;
+        const bool rf32 = e.residual != nullptr && e.residual_dtype == MG_F32;
+        if (y_dtype != MG_BF16)
+            r = rf32 ? launch_tiled<EpFull<float, ACT, true>>(a, st) : launch_tiled<EpFull<float, ACT, false>>(a, st);
+        else if (e.residual || e.gated)
+            r = rf32 ? launch_tiled<EpFull<uint16_t, ACT, true>>(a, st) : launch_tiled<EpFull<uint16_t, ACT, false>>(a, st);
+        else
+            r = launch_tiled<EpBiasAct<ACT>>(a, st);
+    });
+    return r;
 }
 
 }  // namespace mg

@@ -1,0 +1,321 @@
+// The dual GEMM with its epilogue for few token rows, where the 4-bit weights
+// are the traffic and the 256x256 tiles of the large kernel leave most of the
+// chip idle: small output tiles, and K split over the waves of a workgroup.
+//
+// A workgroup takes TG groups of 32 tokens by NG groups of 32 columns; wave w
+// takes every NW-th half-window of K (256 channels: four 64-channel slices,
+// whose scale codes are one 32-bit word per row and half) and every NW-th
+// slice of the outlier columns.  Operands are in fragment order, so a slice of
+// 32 rows is one 16-byte load per lane of 1 KB of contiguous memory straight
+// into the matrix instruction's registers: nothing passes through LDS, no
+// barrier stands in the K loop, and a wave keeps 4 D slices per row group in
+// flight.  Loads of rows past M or N and of slices past K leave the buffers'
+// ranges and read 0.  The waves' partial sums meet in LDS and are added in the
+// order of the waves, so a call's bits do not vary.
+//
+// Bound: one token, K = 5120 -> N = 13824 (35.4 MB of codes, 2.2 MB of scales)
+// takes 9.6 us, 13824 -> 5120 8.9 us, of which a launch and its host call are
+// about 7 (a 1024 x 1024 layer takes 7.9); the 256x256 tiles take 34 and 72.
+// With more tokens the operands' way into a CU bounds it (few_tile).
+#include "gemm_epilogue.h"
+#include "mg_block.h"
+#include "mg_device.h"
+#include "mg_internal.h"
+
+namespace mg {
+
+namespace {
+
+typedef int v8i __attribute__((ext_vector_type(8)));
+typedef float v16f __attribute__((ext_vector_type(16)));
+typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
+
+struct FewArgs {
+    const uint8_t* Aq;
+    const uint8_t* As;
+    const uint16_t* XO;
+    const uint8_t* Wq;
+    const uint8_t* Ws;
+    const uint16_t* WO;
+    void* Y;
+    int64_t M;
+    int32_t N, K, k;
+    EpArgs ep;
+};
+
+template <int OPSEL>
+__device__ __forceinline__ v16f few_fp4(ep_u32x4 w, ep_u32x4 a, uint32_t sw, uint32_t sa, v16f c) {
+    const v8i wv = {(int)w[0], (int)w[1], (int)w[2], (int)w[3], 0, 0, 0, 0};
+    const v8i av = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
+    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(wv, av, c, 4, 4, OPSEL, (int)sw, OPSEL, (int)sa);
+}
+
+// 16 bytes at lane offset voff plus wave offset soff, which always lies inside
+// the buffer; without `ok` the lane offset leaves it and 0 is read.
+__device__ __forceinline__ ep_u32x4 few_load(__amdgpu_buffer_rsrc_t r, bool ok, uint32_t voff, uint32_t soff) {
+    return __builtin_bit_cast(ep_u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, ok ? voff : kEpNowhere, ok ? soff : 0u, 0));
+}
+__device__ __forceinline__ uint32_t few_load1(__amdgpu_buffer_rsrc_t r, bool ok, uint32_t voff, uint32_t soff) {
+    return __builtin_amdgcn_raw_buffer_load_b32(r, ok ? voff : kEpNowhere, ok ? soff : 0u, 0);
+}
+
+// TG groups of 32 tokens by NG groups of 32 columns per workgroup, NW waves
+// that split K, D half-windows in flight per wave.
+template <typename YT, int TG, int NG, int NW, int D>
+__global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW / 4))) gemm_few(FewArgs g) {
+    extern __shared__ __attribute__((aligned(16))) float part[];      // [NW][32][ROW]
+    constexpr bool YF = std::is_same_v<YT, float>;
+    constexpr int ROW = 32 * NG + 4;                                  // floats per staged row
+    constexpr int PR = 8 * NG;                                        // pieces of 4 columns per token
+    constexpr int RS = 64 * NW / PR;                                  // token rows the workgroup takes at once
+    constexpr int PT = RS >= 32 ? 1 : 32 / RS;                        // pieces per thread and token group
+    constexpr bool EARLY = TG == 1 && PT == 1;                        // epilogue inputs loaded ahead of the K loop
+    const int tid = threadIdx.x, lane = tid & 63, l32 = lane & 31, h = lane >> 5;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int K = g.K, N = g.N;
+    const int64_t M = g.M;
+    const EpArgs& e = g.ep;
+    // workgroups go round-robin to the 8 XCDs: XCD x takes column blocks x,
+    // x + 8, ..., each with all its token blocks in a row (they share weights)
+    const int gy = (int)((M + 32 * TG - 1) / (32 * TG)), j = (int)blockIdx.x >> 3;
+    const int bx = ((int)blockIdx.x & 7) + 8 * (j / gy), by = j % gy;
+    const int n0 = bx * 32 * NG;
+    if (n0 >= N) return;
+    const int64_t t0 = (int64_t)by * 32 * TG;
+
+    // ---- the epilogue's inputs: a thread's columns are the same in every row it takes
+    const int prow = tid / PR, pcol = n0 + 4 * (tid % PR);
+    const bool pon = prow < 32 && pcol < N;
+    float bias[4] = {}, gate[PT][4], res[PT][4];
+    int mi[PT];
+    auto ep_inputs = [&](int t) {
+#pragma unroll
+        for (int p = 0; p < PT; ++p) {
+            const int64_t m = t0 + 32 * t + p * RS + prow;
+            const bool on = pon && m < M;
+            mi[p] = on ? mod_row(e.mod, m) : -1;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) { gate[p][c] = 1.0f; res[p][c] = 0.0f; }
+            if (on && e.residual) ep_load4(e.residual, m * e.ldr + pcol, e.residual_dtype == MG_F32, res[p]);
+            if (e.mod.gate && mi[p] >= 0) ep_load4(e.mod.gate, (int64_t)mi[p] * e.mod.ld + pcol, e.mod.dtype == MG_F32, gate[p]);
+        }
+    };
+    if (e.bias && pon) ep_load4(e.bias, pcol, e.bias_dtype == MG_F32, bias);
+    if constexpr (EARLY) ep_inputs(0);
+
+    // ---- this wave's part of K
+    const uint32_t ns4 = (uint32_t)frag_slices(K / 2);
+    const int units = (int)(ns4 + 3) / 4;                             // half-windows
+    const uint32_t nwin = (uint32_t)sc_nwin(K);
+    const __amdgpu_buffer_rsrc_t rA = make_rsrc(g.Aq, (uint64_t)frag_bytes(M, K / 2));
+    const __amdgpu_buffer_rsrc_t rB = make_rsrc(g.Wq, (uint64_t)frag_bytes(N, K / 2));
+    const __amdgpu_buffer_rsrc_t rAs = make_rsrc(g.As, (uint64_t)sc_bytes(M, K));
+    const __amdgpu_buffer_rsrc_t rBs = make_rsrc(g.Ws, (uint64_t)sc_bytes(N, K));
+    const uint32_t l16 = 16u * (uint32_t)lane;
+    uint32_t offA[TG], offAs[TG], offB[NG], offBs[NG];
+#pragma unroll
+    for (int t = 0; t < TG; ++t) {
+        const int64_t m = t0 + 32 * t + l32;                          // absent tokens read 0
+        offA[t] = m < M ? (uint32_t)(m / 32) * ns4 * kFragBlock + l16 : kEpNowhere;
+        offAs[t] = m < M ? (uint32_t)(m / kScRows) * nwin * kScWinBytes + (uint32_t)((m % kScRows) * kScBlocks + 8 * h) : kEpNowhere;
+    }
+#pragma unroll
+    for (int c = 0; c < NG; ++c) {
+        const int n = n0 + 32 * c + l32;
+        offB[c] = n < N ? (uint32_t)(n / 32) * ns4 * kFragBlock + l16 : kEpNowhere;
+        offBs[c] = n < N ? (uint32_t)(n / kScRows) * nwin * kScWinBytes + (uint32_t)((n % kScRows) * kScBlocks + 8 * h) : kEpNowhere;
+    }
+
+    v16f acc[TG][NG];
+#pragma unroll
+    for (int t = 0; t < TG; ++t)
+#pragma unroll
+        for (int c = 0; c < NG; ++c) acc[t][c] = v16f{};
+    ep_u32x4 w[D][NG][4], a[D][TG][4];
+    uint32_t sw[D][NG], sa[D][TG];
+    // slice s of half-window u, and the half-window's scale codes, into
+    // register set d.  Slices past the last read 0 (no memory is touched), so
+    // the loop needs no branches: a wave's surplus half-windows add 0.
+    auto load_slice = [&](int u, int d, int s) {
+        const uint32_t sl = 4u * (uint32_t)u + (uint32_t)s;
+        const bool ok = sl < ns4;
+#pragma unroll
+        for (int c = 0; c < NG; ++c) w[d][c][s] = few_load(rB, ok, offB[c], sl * kFragBlock);
+#pragma unroll
+        for (int t = 0; t < TG; ++t) a[d][t][s] = few_load(rA, ok, offA[t], sl * kFragBlock);
+    };
+    auto load_scales = [&](int u, int d) {
+        const uint32_t so = (uint32_t)(u >> 1) * kScWinBytes + 4u * (u & 1);
+        const bool ok = u < units;
+#pragma unroll
+        for (int c = 0; c < NG; ++c) sw[d][c] = few_load1(rBs, ok, offBs[c], so);
+#pragma unroll
+        for (int t = 0; t < TG; ++t) sa[d][t] = few_load1(rAs, ok, offAs[t], so);
+    };
+    // ---- outlier columns: slices of 16 bf16 values, every NW-th a wave's.
+    // The first is asked for ahead of the bulk and multiplied behind its loads.
+    const uint32_t nso = (uint32_t)frag_slices(2 * (int64_t)g.k);
+    const __amdgpu_buffer_rsrc_t rX = make_rsrc(g.XO, (uint64_t)frag_bytes(M, 2 * (int64_t)g.k));
+    const __amdgpu_buffer_rsrc_t rW = make_rsrc(g.WO, (uint64_t)frag_bytes(N, 2 * (int64_t)g.k));
+    ep_u32x4 ww[NG], x[TG];
+    auto load_outlier = [&](uint32_t s) {
+#pragma unroll
+        for (int c = 0; c < NG; ++c)
+            ww[c] = few_load(rW, n0 + 32 * c < N, l16, ((uint32_t)(n0 / 32 + c) * nso + s) * kFragBlock);
+#pragma unroll
+        for (int t = 0; t < TG; ++t)
+            x[t] = few_load(rX, t0 + 32 * t < M, l16, (((uint32_t)(t0 / 32) + t) * nso + s) * kFragBlock);
+    };
+    auto use_outlier = [&]() {
+#pragma unroll
+        for (int t = 0; t < TG; ++t)
+#pragma unroll
+            for (int c = 0; c < NG; ++c)
+                acc[t][c] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(v8bf, ww[c]),
+                                                                    __builtin_bit_cast(v8bf, x[t]), acc[t][c], 0, 0, 0);
+    };
+    if ((uint32_t)wave < nso) load_outlier((uint32_t)wave);
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
+        load_scales(wave + d * NW, d);
+#pragma unroll
+        for (int s = 0; s < 4; ++s) load_slice(wave + d * NW, d, s);
+    }
+    if ((uint32_t)wave < nso) use_outlier();
+    for (uint32_t s = (uint32_t)wave + NW; s < nso; s += NW) {
+        load_outlier(s);
+        use_outlier();
+    }
+    // D half-windows of the wave, refilling each slice's registers (REFILL) as
+    // soon as it is multiplied
+    int u0 = wave;
+    auto round = [&](auto REFILL) {
+#pragma unroll
+        for (int d = 0; d < D; ++d) {
+            const int next = u0 + (d + D) * NW;
+            // the next scale codes are asked for ahead of the next slices, so
+            // that waiting for them does not wait for those
+            uint32_t cw[NG], ca[TG];
+#pragma unroll
+            for (int c = 0; c < NG; ++c) cw[c] = sw[d][c];
+#pragma unroll
+            for (int t = 0; t < TG; ++t) ca[t] = sa[d][t];
+            if constexpr (decltype(REFILL)::value) load_scales(next, d);
+            auto slice = [&](auto S) {
+                constexpr int s = decltype(S)::value;
+#pragma unroll
+                for (int t = 0; t < TG; ++t)
+#pragma unroll
+                    for (int c = 0; c < NG; ++c)
+                        acc[t][c] = few_fp4<s>(w[d][c][s], a[d][t][s], cw[c], ca[t], acc[t][c]);
+                if constexpr (decltype(REFILL)::value) {
+                    load_slice(next, d, s);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            };
+            slice(std::integral_constant<int, 0>{});
+            slice(std::integral_constant<int, 1>{});
+            slice(std::integral_constant<int, 2>{});
+            slice(std::integral_constant<int, 3>{});
+        }
+    };
+    for (; u0 + D * NW < units; u0 += D * NW) round(std::true_type{});
+    round(std::false_type{});
+    // ---- join and epilogue, one token group at a time: register 4 q + i of
+    // lane (l32, h) is token l32, column 8 q + 4 h + i of its 32
+#pragma unroll
+    for (int t = 0; t < TG; ++t) {
+        if constexpr (!EARLY) ep_inputs(t);
+        if (t > 0) __syncthreads();                                   // the sums of the last group are taken
+#pragma unroll
+        for (int c = 0; c < NG; ++c)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                *reinterpret_cast<ep_f32x4*>(part + (size_t)(wave * 32 + l32) * ROW + 32 * c + 8 * q + 4 * h) =
+                    ep_f32x4{acc[t][c][4 * q], acc[t][c][4 * q + 1], acc[t][c][4 * q + 2], acc[t][c][4 * q + 3]};
+        __syncthreads();
+#pragma unroll
+        for (int p = 0; p < PT; ++p) {
+            const int64_t m = t0 + 32 * t + p * RS + prow;
+            if (!pon || m >= M) continue;
+            float v[4] = {};
+#pragma unroll
+            for (int x = 0; x < NW; ++x) {
+                const ep_f32x4 s = *reinterpret_cast<const ep_f32x4*>(part + (size_t)(x * 32 + p * RS + prow) * ROW + 4 * (tid % PR));
+#pragma unroll
+                for (int c = 0; c < 4; ++c) v[c] += s[c];
+            }
+            ep_by_act(e.act, [&](auto A) {
+#pragma unroll
+                for (int c = 0; c < 4; ++c) v[c] = ep_act<decltype(A)::value>(v[c] + bias[c]);
+            });
+#pragma unroll
+            for (int c = 0; c < 4; ++c) v[c] = mi[p] < 0 ? res[p][c] : __builtin_fmaf(gate[p][c], v[c], res[p][c]);
+            YT* y = static_cast<YT*>(g.Y) + m * N + pcol;
+            if constexpr (YF) *reinterpret_cast<ep_f32x4*>(y) = ep_f32x4{v[0], v[1], v[2], v[3]};
+            else *reinterpret_cast<ep_u32x2*>(y) = ep_u32x2{ep_pack(v[0], v[1]), ep_pack(v[2], v[3])};
+        }
+    }
+}
+
+template <typename YT, int TG, int NG, int NW, int D>
+hipError_t launch_few(const FewArgs& a, hipStream_t st) {
+    constexpr int lds = NW * 32 * (32 * NG + 4) * 4;
+    static thread_local int configured_dev = -1;
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess) return hipErrorNoDevice;
+    if (configured_dev != dev) {
+        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&gemm_few<YT, TG, NG, NW, D>),
+                                                 hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+        if (e != hipSuccess) return e;
+        configured_dev = dev;
+    }
+    const int64_t gx = (a.N + 32 * NG - 1) / (32 * NG), gy = (a.M + 32 * TG - 1) / (32 * TG);
+    hipLaunchKernelGGL((gemm_few<YT, TG, NG, NW, D>), dim3((unsigned)((gx + 7) / 8 * 8 * gy)), dim3(64 * NW), lds, st, a);
+    return hipGetLastError();
+}
+
+template <typename YT>
+hipError_t run_few(int tile, const FewArgs& a, hipStream_t st) {
+    switch (tile) {
+        case 0: return launch_few<YT, 1, 1, 8, 3>(a, st);
+        case 1: return launch_few<YT, 2, 1, 8, 2>(a, st);
+        case 2: return launch_few<YT, 2, 2, 8, 2>(a, st);
+        case 3: return launch_few<YT, 2, 2, 4, 2>(a, st);
+        case 4: return launch_few<YT, 4, 2, 8, 1>(a, st);
+        default: return launch_few<YT, 4, 4, 4, 1>(a, st);
+    }
+}
+
+}  // namespace
+
+int few_tile(int64_t M, int32_t N, int32_t K) {
+    // A CU takes in about 57 bytes a nanosecond, from L2 or beyond, whatever
+    // the tile: measured times follow the operand bytes of a workgroup times
+    // the workgroups per CU, plus what a workgroup spends outside its K loop.
+    static const struct { int tg, ng; double own; } tiles[] = {{1, 1, 1.0}, {2, 1, 1.5}, {2, 2, 2.0}, {2, 2, 2.0}, {4, 2, 3.0}, {4, 4, 10.0}};
+    const double cus = device_cu_count(), row = 16.0 * K / 57e3;      // us for 32 rows of K channels
+    const int64_t big = ((M + 255) / 256) * ((N + 255) / 256);
+    double best = (double)(int64_t)((big + cus - 1) / cus) * (16 * row + 8.0) + 4.0;
+    int tile = -1;
+    for (int i = 0; i < 6; ++i) {
+        const int64_t wgs = ((M + 32 * tiles[i].tg - 1) / (32 * tiles[i].tg)) * ((N + 32 * tiles[i].ng - 1) / (32 * tiles[i].ng));
+        if (i == 2 ? wgs > cus : i == 3 ? wgs <= cus : false) continue;   // 8 waves if alone on a CU, else two of 4
+        const double rounds = wgs > 2 * cus ? wgs / cus : wgs > cus ? 2.0 : 1.0;
+        const double t = rounds * ((tiles[i].tg + tiles[i].ng) * row + tiles[i].own);
+        if (t < best) {
+            best = t;
+            tile = i;
+        }
+    }
+    return tile;
+}
+
+hipError_t launch_dual_gemm_few(const uint8_t* Aq, const uint8_t* As, const uint16_t* XO, const uint8_t* Wq,
+                                const uint8_t* Ws, const uint16_t* WO, int64_t M, int32_t N, int32_t K, int32_t k,
+                                const EpArgs& e, void* Y, int32_t y_dtype, int tile, hipStream_t st) {
+    const FewArgs a{Aq, As, XO, Wq, Ws, WO, Y, M, N, K, k, e};
+    return y_dtype == MG_F32 ? run_few<float>(tile, a, st) : run_few<uint16_t>(tile, a, st);
+}
+
+}  // namespace mg
