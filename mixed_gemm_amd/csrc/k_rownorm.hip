@@ -10,6 +10,10 @@
 // own mean, and the waves' (sum, squares) pairs are joined by the parallel
 // variance formula (T. Chan, G. Golub, R. LeVeque, 1983), so one exchange
 // through LDS serves both.
+//
+// Rows may start at any element and have any width from 8 on: loads are
+// unaligned 16-byte loads, and a thread at the row's end loads the row's last
+// 8 channels and shifts them into place, so that no load needs a branch.
 #include <type_traits>
 
 #include "mg_block.h"
@@ -25,48 +29,43 @@ struct __attribute__((packed, aligned(2))) Piece16 { u32x4 v; };   // 16 bytes a
 
 constexpr int kMaxWaves = 16;
 
-// Sum over the wave's 64 lanes, in every lane: DPP adds inside rows of 16,
-// then across the rows into lane 63.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_add(float v) {
+    return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, ROWS, 0xF, true));
+}
+// Sum over each row of 16 lanes, in every lane of the row.
+__device__ __forceinline__ float row16_sum(float v) {
+    v = dpp_add<0xB1, 0xF>(v);         // lane ^ 1
+    v = dpp_add<0x4E, 0xF>(v);         // lane ^ 2
+    v = dpp_add<0x141, 0xF>(v);        // mirror in 8
+    return dpp_add<0x140, 0xF>(v);     // mirror in 16
+}
+// Sum over the wave, wave-uniform.
 __device__ __forceinline__ float wave_sum(float v) {
-    auto dpp = [](float x, auto ctrl, auto rows) {
-        return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), decltype(ctrl)::value,
-                                                          decltype(rows)::value, 0xF, true));
-    };
-#define MG_DPP_ADD(ctrl, rows) v += dpp(v, std::integral_constant<int, ctrl>{}, std::integral_constant<int, rows>{})
-    MG_DPP_ADD(0xB1, 0xF);     // lane ^ 1
-    MG_DPP_ADD(0x4E, 0xF);     // lane ^ 2
-    MG_DPP_ADD(0x141, 0xF);    // mirror in 8
-    MG_DPP_ADD(0x140, 0xF);    // mirror in 16
-    MG_DPP_ADD(0x142, 0xA);    // row 0 -> 1, 2 -> 3
-    MG_DPP_ADD(0x143, 0xC);    // rows 0-1 -> 2, 3
-#undef MG_DPP_ADD
+    v = row16_sum(v);
+    v = dpp_add<0x142, 0xA>(v);        // row 0 -> 1, 2 -> 3
+    v = dpp_add<0x143, 0xC>(v);        // rows 0-1 -> 2, 3
     return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
 }
 
-// 8 consecutive elements from p on, of which `left` exist (the rest read as 0).
-__device__ __forceinline__ void load8(const uint16_t* p, int left, float (&v)[8]) {
-    if (left >= 8) {
-        const u32x4 w = reinterpret_cast<const Piece16*>(p)->v;
+// 8 consecutive elements as they lie in memory: T float or uint16_t (bf16).
+template <typename T>
+struct Raw8 {
+    u32x4 d[sizeof(T) / 2];
+};
+template <typename T>
+__device__ __forceinline__ void load_raw(const T* p, Raw8<T>& r) {
+    constexpr int N = sizeof(T) / 2;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = __uint_as_float(i & 1 ? w[i >> 1] & 0xFFFF0000u : w[i >> 1] << 16);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = i < left ? bf16_to_f32(p[i]) : 0.0f;
-    }
+    for (int i = 0; i < N; ++i) r.d[i] = reinterpret_cast<const Piece16*>(p + 8 / N * i)->v;
 }
-__device__ __forceinline__ void load8(const float* p, int left, float (&v)[8]) {
-    if (left >= 8) {
-        const u32x4 a = reinterpret_cast<const Piece16*>(p)->v, b = reinterpret_cast<const Piece16*>(p + 4)->v;
+template <typename T>
+__device__ __forceinline__ void unpack(const Raw8<T>& r, float (&v)[8]) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) { v[i] = __uint_as_float(a[i]); v[4 + i] = __uint_as_float(b[i]); }
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = i < left ? p[i] : 0.0f;
+    for (int i = 0; i < 8; ++i) {
+        if constexpr (sizeof(T) == 4) v[i] = __uint_as_float(r.d[i >> 2][i & 3]);
+        else v[i] = __uint_as_float(i & 1 ? r.d[0][i >> 1] & 0xFFFF0000u : r.d[0][i >> 1] << 16);
     }
-}
-__device__ __forceinline__ void load8(const void* p, int64_t at, int32_t dtype, int left, float (&v)[8]) {
-    if (dtype == MG_F32) load8(static_cast<const float*>(p) + at, left, v);
-    else load8(static_cast<const uint16_t*>(p) + at, left, v);
 }
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
@@ -76,244 +75,604 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const f32x2 v = {lo, hi};
     return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, bf16x2));
 }
-
-__device__ __forceinline__ void store8(void* p, int64_t at, int32_t dtype, int left, const float (&v)[8]) {
-    if (left <= 0) return;
-    if (dtype == MG_F32) {
-        float* q = static_cast<float*>(p) + at;
-        if (left >= 8) {
-            u32x4 a, b;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) { a[i] = __float_as_uint(v[i]); b[i] = __float_as_uint(v[4 + i]); }
-            reinterpret_cast<Piece16*>(q)->v = a;
-            reinterpret_cast<Piece16*>(q + 4)->v = b;
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i < left) q[i] = v[i];
-        }
-    } else {
-        uint16_t* q = static_cast<uint16_t*>(p) + at;
-        const u32x4 w = {pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
-        if (left >= 8) {
-            reinterpret_cast<Piece16*>(q)->v = w;
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-                if (i < left) q[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
-        }
-    }
+__device__ __forceinline__ u32x4 pack8_bf16(const float (&v)[8]) {
+    return u32x4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
 }
 
-// Elements of wave w's channels below K.
-__device__ __forceinline__ int wave_count(int w, int V, int T, int K) {
-    int n = 0;
-    for (int v = 0; v < V; ++v) {
-        const int left = K - 8 * (v * T + 64 * w);
-        n += left < 0 ? 0 : left < 512 ? left : 512;
-    }
-    return n;
-}
-
+// A thread's place in rows of K >= 8 channels: V vectors, W waves.
 template <int V>
 struct RowThread {
-    int W, T, wave, K;
+    int W, T, wave, K, shift;       // shift: channels missing in the row's last vector
     int col[V];                     // first channel of vector v
-    int n;                          // channels of this wave
-    float rn;
-    bool whole;                     // every lane of the wave has all its channels
+    int at[V];                      // where its 8 elements are loaded from (the row's last 8 past col = K - 8)
+    uint32_t full, cut;             // bit v: the wave's vector lies inside the row; holds its last, partial vector
+    float rn, rK;                   // 1 / channels of this wave, 1 / K
+    float nl, rnl;                  // channels of wave (lane % 16), 1 / them (0 past the last wave)
 
     __device__ __forceinline__ RowThread(int K_) : K(K_) {
         T = blockDim.x;
         W = T >> 6;
         wave = __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
+        shift = (8 - (K & 7)) & 7;
+        full = cut = 0;
 #pragma unroll
-        for (int v = 0; v < V; ++v) col[v] = 8 * (v * T + (int)threadIdx.x);
-        n = wave_count(wave, V, T, K);
-        rn = n ? 1.0f / (float)n : 0.0f;
-        whole = n == 512 * V;
+        for (int v = 0; v < V; ++v) {
+            col[v] = 8 * (v * T + (int)threadIdx.x);
+            at[v] = col[v] < K - 8 ? col[v] : K - 8;
+            const int l = K - 8 * (v * T + 64 * wave);
+            full |= (l >= 512 ? 1u : 0u) << v;
+            cut |= (shift && l > 0 && l < 512 ? 1u : 0u) << v;
+        }
+        auto count = [&](int w) {
+            int c = 0;
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int l = K - 8 * (v * T + 64 * w);
+                c += l < 0 ? 0 : l < 512 ? l : 512;
+            }
+            return c;
+        };
+        const int c = count(wave), cl = (int)(threadIdx.x & 15) < W ? count((int)threadIdx.x & 15) : 0;
+        rn = c ? 1.0f / (float)c : 0.0f;
+        nl = (float)cl;
+        rnl = cl ? 1.0f / (float)cl : 0.0f;
+        rK = 1.0f / (float)K;
     }
     __device__ __forceinline__ int left(int v) const { return K - col[v]; }
+    __device__ __forceinline__ bool whole() const { return full == (1u << V) - 1u; }
+    // Values loaded at at[v] moved to the vector's own channels (those past the
+    // row hold anything: they are counted nowhere and never stored).
+    __device__ __forceinline__ void place(int v, float (&x)[8]) const {
+        if (cut >> v & 1u) {
+            const bool me = col[v] < K && col[v] > K - 8;
+            for (int k = 0; k < shift; ++k) {
+#pragma unroll
+                for (int i = 0; i < 7; ++i) x[i] = me ? x[i + 1] : x[i];
+            }
+        }
+    }
+    // 8 values of a [K] array of either type
+    __device__ __forceinline__ void load8(const void* p, int64_t row, int32_t dtype, int v, float (&x)[8]) const {
+        if (dtype == MG_F32) {
+            Raw8<float> r;
+            load_raw(static_cast<const float*>(p) + row + at[v], r);
+            unpack(r, x);
+        } else {
+            Raw8<uint16_t> r;
+            load_raw(static_cast<const uint16_t*>(p) + row + at[v], r);
+            unpack(r, x);
+        }
+        place(v, x);
+    }
+    __device__ __forceinline__ void store8(void* p, int64_t row, int32_t dtype, int v, const float (&x)[8]) const {
+        const bool f32 = dtype == MG_F32;
+        float* const pf = static_cast<float*>(p) + row + col[v];
+        uint16_t* const pb = static_cast<uint16_t*>(p) + row + col[v];
+        auto piece = [&]() {
+            if (f32) {
+                u32x4 a, b;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) { a[i] = __float_as_uint(x[i]); b[i] = __float_as_uint(x[4 + i]); }
+                reinterpret_cast<Piece16*>(pf)->v = a;
+                reinterpret_cast<Piece16*>(pf + 4)->v = b;
+            } else {
+                reinterpret_cast<Piece16*>(pb)->v = pack8_bf16(x);
+            }
+        };
+        if (full >> v & 1u) {
+            piece();
+        } else if (left(v) >= 8) {
+            piece();
+        } else {
+            const int l = left(v);
+            const u32x4 w = pack8_bf16(x);
+#pragma unroll
+            for (int i = 0; i < 7; ++i)
+                if (i < l) {
+                    if (f32) pf[i] = x[i];
+                    else pb[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+                }
+        }
+    }
 };
 
-// mean (0 for rms) and 1 / sqrt(var + eps) of the row x.  The waves exchange
-// (sum, squared deviations from the wave's mean) through one slot each of two
-// sets used in turn, so that one barrier suffices: a wave writes a set again
-// only after the barrier of the other, which every reader of the set has
-// passed.
+// The waves' (sum, squared deviations from the wave's mean) of a row, two sets
+// used in turn so that one barrier suffices: a wave writes a set again only
+// after the barrier of the other, which every reader of the set has passed.
+typedef f32x2 Pairs[2][kMaxWaves];
+
+// 1 / sqrt(v), v >= 0 (the hardware's, one unit in the last place; subnormal v
+// scaled into its range)
+__device__ __forceinline__ float rsqrt_f32(float v) {
+    const bool tiny = v < 0x1p-100f;
+    const float r = __builtin_amdgcn_rsqf(tiny ? v * 0x1p100f : v);
+    return tiny ? r * 0x1p50f : r;
+}
+
+// mean (0 for rms) and 1 / sqrt(var + eps) of the row x: the parallel variance
+// formula over the waves, whose pairs the 16 lanes of a row take one each.
 template <int V>
-__device__ __forceinline__ void row_stats(const float (&x)[V][8], const RowThread<V>& t, const NormArgs& nm, f32x2 (*pair)[kMaxWaves],
+__device__ __forceinline__ void row_stats(const float (&x)[V][8], const RowThread<V>& t, int kind, float eps, Pairs& pairs,
                                           int& turn, float& mean, float& rstd) {
     float s = 0.0f, m = 0.0f, q = 0.0f;
-    if (nm.kind == MG_NORM_LAYER) {
+    const bool layer = kind == MG_NORM_LAYER;
+    if (t.whole()) {
+        if (layer) {
+#pragma unroll
+            for (int v = 0; v < V; ++v)
+#pragma unroll
+                for (int i = 0; i < 8; ++i) s += x[v][i];
+            s = wave_sum(s);
+            m = s * t.rn;
+        }
 #pragma unroll
         for (int v = 0; v < V; ++v)
 #pragma unroll
-            for (int i = 0; i < 8; ++i) s += x[v][i];
-        s = wave_sum(s);
-        m = s * t.rn;
-    }
+            for (int i = 0; i < 8; ++i) {
+                const float d = x[v][i] - m;
+                q = __builtin_fmaf(d, d, q);
+            }
+    } else {
+        if (layer) {
 #pragma unroll
-    for (int v = 0; v < V; ++v)
+            for (int v = 0; v < V; ++v)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const float d = t.whole || i < t.left(v) ? x[v][i] - m : 0.0f;
-            q = __builtin_fmaf(d, d, q);
+                for (int i = 0; i < 8; ++i) s += i < t.left(v) ? x[v][i] : 0.0f;
+            s = wave_sum(s);
+            m = s * t.rn;
         }
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float d = i < t.left(v) ? x[v][i] - m : 0.0f;
+                q = __builtin_fmaf(d, d, q);
+            }
+    }
     q = wave_sum(q);
-    f32x2* set = pair[turn];
+    f32x2* set = pairs[turn];
     turn ^= 1;
     if ((threadIdx.x & 63) == 0) set[t.wave] = f32x2{s, q};
     __syncthreads();
-    float S = 0.0f, Q = 0.0f;
-    for (int w = 0; w < t.W; ++w) S += set[w][0];
-    mean = S / (float)t.K;
-    for (int w = 0; w < t.W; ++w) {
-        const float nw = (float)wave_count(w, V, t.T, t.K);
-        const float d = nw > 0.0f ? set[w][0] / nw - mean : 0.0f;
-        Q += set[w][1] + nw * d * d;
-    }
-    rstd = 1.0f / __fsqrt_rn(Q / (float)t.K + nm.eps);
+    const int l = (int)threadIdx.x & 15;
+    const f32x2 p = l < t.W ? set[l] : f32x2{0.0f, 0.0f};
+    mean = layer ? row16_sum(p[0]) * t.rK : 0.0f;
+    const float d = p[0] * t.rnl - mean;
+    const float Q = row16_sum(__builtin_fmaf(t.nl * d, d, p[1]));
+    rstd = rsqrt_f32(__builtin_fmaf(Q, t.rK, eps));
 }
 
-// v = ((x - mean) rstd) w + b of 8 channels
-__device__ __forceinline__ void norm8(float (&x)[8], int64_t col, int left, const NormArgs& n, float mean, float rstd) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = (x[i] - mean) * rstd;
-    float c[8];
-    if (n.weight) {
-        load8(n.weight, col, n.dtype, left, c);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] *= c[i];
-    }
-    if (n.bias) {
-        load8(n.bias, col, n.dtype, left, c);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] += c[i];
-    }
-}
-
-// x (1 + scale_i) + shift_i, or 0 on a padding row
-__device__ __forceinline__ void mod8(float (&x)[8], int64_t col, int left, const ModArgs& m, int row) {
-    float c[8];
-    if (row < 0) {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = 0.0f;
-        return;
-    }
-    if (m.scale) {
-        load8(m.scale, row * m.ld + col, m.dtype, left, c);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] *= 1.0f + c[i];
-    }
-    if (m.shift) {
-        load8(m.shift, row * m.ld + col, m.dtype, left, c);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] += c[i];
-    }
-}
-
+// A norm with its modulation folded to n a + c, n = (x - mean) rstd: a = w (1 +
+// scale_i), c = b (1 + scale_i) + shift_i of 8 channels.
 template <int V>
-__global__ void __launch_bounds__(64 * kMaxWaves) row_kernel(RowArgs a) {
-    __shared__ f32x2 pair[2][kMaxWaves];
+__device__ __forceinline__ void fold8(const RowThread<V>& t, const NormArgs& n, const ModArgs& m, int row, int v,
+                                      float (&a)[8], float (&c)[8]) {
+    float w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) { a[i] = 1.0f; c[i] = 0.0f; }
+    if (m.scale) {
+        t.load8(m.scale, row * m.ld, m.dtype, v, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) a[i] = 1.0f + w[i];
+    }
+    if (m.shift) t.load8(m.shift, row * m.ld, m.dtype, v, c);
+    if (n.bias) {
+        t.load8(n.bias, 0, n.dtype, v, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) c[i] = __builtin_fmaf(w[i], a[i], c[i]);
+    }
+    if (n.weight) {
+        t.load8(n.weight, 0, n.dtype, v, w);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) a[i] *= w[i];
+    }
+}
+// n a + c; the rounding of -mean rstd is as small as the mean's own
+__device__ __forceinline__ void apply8(float (&x)[8], float mean, float rstd, const float (&a)[8], const float (&c)[8]) {
+    const float b = -mean * rstd;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = __builtin_fmaf(__builtin_fmaf(x[i], rstd, b), a[i], c[i]);
+}
+// The norm after the block (weight pw; the rare bias is read where it is used).
+template <int V>
+__device__ __forceinline__ void post8(const RowThread<V>& t, float (&y)[8], const NormArgs& n, const float (&pw)[8], int v,
+                                      float mean, float rstd) {
+    const float b = -mean * rstd;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = __builtin_fmaf(y[i], rstd, b) * pw[i];
+    if (n.bias) {
+        float c[8];
+        t.load8(n.bias, 0, n.dtype, v, c);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] += c[i];
+    }
+}
+// 8 values of an optional array (1 without one)
+template <int V>
+__device__ __forceinline__ void load_or_1(const RowThread<V>& t, const void* p, int64_t row, int32_t dtype, int v, float (&g)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) g[i] = 1.0f;
+    if (p) t.load8(p, row, dtype, v, g);
+}
+
+// The rows of a workgroup, r0 + i step for i < count: consecutive where token
+// rows of a sample share a modulation row, else spread over the workgroups.
+struct RowSpan {
+    int64_t chunk, step;        // rows per workgroup; 1, or the number of workgroups
+};
+
+template <int V, typename XT, typename YT>
+struct RowShape {
+    static constexpr bool res = !std::is_void_v<YT>, ahead = V <= 4, keep = res ? V <= 2 : V <= 4;
+    using Y = std::conditional_t<res, YT, uint16_t>;
+    static constexpr int waves = V > 4 ? 4 : V == 4 ? 2 : V == 2 ? (res ? 2 : 4) : (res ? 4 : 5);    // per SIMD
+};
+
+// While a row is worked on, the next one's loads are in flight.  Up to 16384
+// channels (8192 with a residual) the folded coefficients, the gate and the
+// weights of the norm after the block stay in registers until the modulation
+// row changes; wider rows read them per row.  XT, YT: types of X and Y (YT
+// void: no residual step).
+template <int V, typename XT, typename YT>
+__global__ void __launch_bounds__(V <= 4 ? 512 : 1024) __attribute__((amdgpu_waves_per_eu(RowShape<V, XT, YT>::waves)))
+row_kernel(RowArgs a, RowSpan span) {
+    using S = RowShape<V, XT, YT>;
+    constexpr bool RES = S::res, KEEP = S::keep;
+    using Y = typename S::Y;
+    __shared__ Pairs pairs;
     int turn = 0;
     const RowThread<V> t(a.K);
-    for (int64_t r = blockIdx.x; r < a.M; r += gridDim.x) {
-        const int gi = mod_row(a.gate, r), mi = mod_row(a.mod, r);
-        float x[V][8];
+    const XT* X = static_cast<const XT*>(a.X);
+    const Y* Yp = static_cast<const Y*>(a.Y);
+    float na[KEEP ? V : 1][8], nc[KEEP ? V : 1][8], ga[KEEP && RES ? V : 1][8], pw[KEEP && RES ? V : 1][8];
+    int mi_of = -1, gi_of = -1;       // modulation rows that the kept coefficients belong to
+    Raw8<XT> rx[V];
+    Raw8<Y> ry[RES ? V : 1];
+    int mrow = -1, grow = -1;         // modulation rows of the row ahead
+    int64_t r = span.step == 1 ? blockIdx.x * span.chunk : blockIdx.x;
+    const int64_t last = span.step == 1 ? (r + span.chunk < a.M ? r + span.chunk : a.M) - 1 : a.M - 1;
+    auto load_row = [&](int64_t r) {
 #pragma unroll
-        for (int v = 0; v < V; ++v) load8(a.X, r * a.ldx + t.col[v], a.x_dtype, t.left(v), x[v]);
-        if (a.Y) {
-            float y[V][8];
-#pragma unroll
-            for (int v = 0; v < V; ++v) load8(a.Y, r * a.ldy + t.col[v], a.y_dtype, t.left(v), y[v]);
-            if (a.has_post) {
-                float mean, rstd;
-                row_stats<V>(y, t, a.post, pair, turn, mean, rstd);
-#pragma unroll
-                for (int v = 0; v < V; ++v) norm8(y[v], t.col[v], t.left(v), a.post, mean, rstd);
-            }
-            if (gi >= 0) {
-#pragma unroll
-                for (int v = 0; v < V; ++v) {
-                    float c[8] = {1, 1, 1, 1, 1, 1, 1, 1};
-                    if (a.gate.gate) load8(a.gate.gate, gi * a.gate.ld + t.col[v], a.gate.dtype, t.left(v), c);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) x[v][i] = t.whole || i < t.left(v) ? __builtin_fmaf(c[i], y[v][i], x[v][i]) : 0.0f;
-                }
-            }
-#pragma unroll
-            for (int v = 0; v < V; ++v) store8(a.O, r * a.ldo + t.col[v], a.x_dtype, t.left(v), x[v]);
+        for (int v = 0; v < V; ++v) {
+            load_raw(X + r * a.ldx + t.at[v], rx[v]);
+            if constexpr (RES) load_raw(Yp + r * a.ldy + t.at[v], ry[v]);
         }
-        if (a.has_norm) {
-            float mean, rstd;
-            row_stats<V>(x, t, a.norm, pair, turn, mean, rstd);
+        if (!RES || a.has_norm) mrow = mod_row(a.mod, r);
+        if constexpr (RES) grow = mod_row(a.gate, r);
+    };
+    if constexpr (KEEP && RES) {
+        if (a.has_post) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) load_or_1(t, a.post.weight, 0, a.post.dtype, v, pw[v]);
+        }
+    }
+    load_row(r);
+    while (true) {
+        const int mi = __builtin_amdgcn_readfirstlane(mrow), gi = __builtin_amdgcn_readfirstlane(grow);
+        if constexpr (KEEP) {
+            if (RES && gi >= 0 && gi != gi_of) {
+#pragma unroll
+                for (int v = 0; v < V; ++v) load_or_1(t, a.gate.gate, gi * a.gate.ld, a.gate.dtype, v, ga[RES ? v : 0]);
+                gi_of = gi;
+            }
+            if (mi >= 0 && mi != mi_of) {
+#pragma unroll
+                for (int v = 0; v < V; ++v) fold8(t, a.norm, a.mod, mi, v, na[v], nc[v]);
+                mi_of = mi;
+            }
+        }
+        float x[V][8], y[RES ? V : 1][8];
+#pragma unroll
+        for (int v = 0; v < V; ++v) {
+            unpack(rx[v], x[v]);
+            t.place(v, x[v]);
+            if constexpr (RES) {
+                unpack(ry[v], y[v]);
+                t.place(v, y[v]);
+            }
+        }
+        const int64_t next = r + span.step;
+        // past the last row it is loaded once more, without a branch
+        if constexpr (S::ahead) load_row(next <= last ? next : last);
+        if constexpr (RES) {
+            float mean = 0.0f, rstd = 1.0f;
+            if (a.has_post) row_stats<V>(y, t, a.post.kind, a.post.eps, pairs, turn, mean, rstd);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                norm8(x[v], t.col[v], t.left(v), a.norm, mean, rstd);
-                mod8(x[v], t.col[v], t.left(v), a.mod, mi);
-                store8(a.H, r * a.ldh + t.col[v], a.h_dtype, t.left(v), x[v]);
+                if (gi >= 0) {
+                    if (a.has_post) {
+                        if constexpr (!KEEP) load_or_1(t, a.post.weight, 0, a.post.dtype, v, pw[0]);
+                        post8(t, y[v], a.post, pw[KEEP ? v : 0], v, mean, rstd);
+                    }
+                    if constexpr (!KEEP) load_or_1(t, a.gate.gate, gi * a.gate.ld, a.gate.dtype, v, ga[0]);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[v][i] = __builtin_fmaf(ga[KEEP ? v : 0][i], y[v][i], x[v][i]);
+                }
+                t.store8(a.O, r * a.ldo, a.x_dtype, v, x[v]);
             }
+        }
+        if (!RES || a.has_norm) {
+            float mean, rstd;
+            row_stats<V>(x, t, a.norm.kind, a.norm.eps, pairs, turn, mean, rstd);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                if (mi >= 0) {
+                    if constexpr (!KEEP) fold8(t, a.norm, a.mod, mi, v, na[0], nc[0]);
+                    apply8(x[v], mean, rstd, na[KEEP ? v : 0], nc[KEEP ? v : 0]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) x[v][i] = 0.0f;
+                }
+                t.store8(a.H, r * a.ldh, a.h_dtype, v, x[v]);
+            }
+        }
+        r = next;
+        if (r > last) break;
+        if constexpr (!S::ahead) load_row(r);
+    }
+}
+
+// Rows of fewer than 8 channels: a thread takes a row.
+__global__ void __launch_bounds__(256) row_small_kernel(RowArgs a) {
+    const int64_t r = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (r >= a.M) return;
+    const int K = a.K;
+    auto stats = [&](const float (&x)[7], const NormArgs& n, float& mean, float& rstd) {
+        float s = 0.0f, q = 0.0f;
+        for (int j = 0; j < K; ++j) s += x[j];
+        mean = n.kind == MG_NORM_LAYER ? s / (float)K : 0.0f;
+        for (int j = 0; j < K; ++j) q = __builtin_fmaf(x[j] - mean, x[j] - mean, q);
+        rstd = rsqrt_f32(q / (float)K + n.eps);
+    };
+    auto normed = [&](float x, int j, const NormArgs& n, float mean, float rstd) {
+        x = (x - mean) * rstd;
+        if (n.weight) x *= load_elem(n.weight, j, n.dtype);
+        return n.bias ? x + load_elem(n.bias, j, n.dtype) : x;
+    };
+    auto put = [&](void* p, int64_t at, int32_t dtype, float v) {
+        if (dtype == MG_F32) static_cast<float*>(p)[at] = v;
+        else static_cast<uint16_t*>(p)[at] = (uint16_t)pack_bf16(v, 0.0f);
+    };
+    float x[7], y[7], mean, rstd;
+    for (int j = 0; j < K; ++j) x[j] = load_elem(a.X, r * a.ldx + j, a.x_dtype);
+    if (a.Y) {
+        const int gi = mod_row(a.gate, r);
+        for (int j = 0; j < K; ++j) y[j] = load_elem(a.Y, r * a.ldy + j, a.y_dtype);
+        if (a.has_post) stats(y, a.post, mean, rstd);
+        for (int j = 0; j < K; ++j) {
+            if (gi >= 0) {
+                const float b = a.has_post ? normed(y[j], j, a.post, mean, rstd) : y[j];
+                x[j] = __builtin_fmaf(a.gate.gate ? load_elem(a.gate.gate, gi * a.gate.ld + j, a.gate.dtype) : 1.0f, b, x[j]);
+            }
+            put(a.O, r * a.ldo + j, a.x_dtype, x[j]);
+        }
+    }
+    if (a.has_norm) {
+        const int mi = mod_row(a.mod, r);
+        stats(x, a.norm, mean, rstd);
+        for (int j = 0; j < K; ++j) {
+            float h = 0.0f;
+            if (mi >= 0) {
+                h = normed(x[j], j, a.norm, mean, rstd);
+                if (a.mod.scale) h *= 1.0f + load_elem(a.mod.scale, mi * a.mod.ld + j, a.mod.dtype);
+                if (a.mod.shift) h += load_elem(a.mod.shift, mi * a.mod.ld + j, a.mod.dtype);
+            }
+            put(a.H, r * a.ldh + j, a.h_dtype, h);
         }
     }
 }
 
-template <int V>
-__global__ void __launch_bounds__(64 * kMaxWaves) norm_quant_kernel(NormQuantArgs g) {
-    __shared__ f32x2 pair[2][kMaxWaves];
+// Per-thread constants of the quantize step for 8 channels: the smoothing
+// scales s, their reciprocals with 0 on outlier channels (whose bulk quotient
+// is then +-0 and whose codes nkeep clears), and the first outlier channel.
+struct QuantLane {
+    float s[8], rz[8];
+    float so, ro, lim;              // the first outlier's s and 1 / s; bound of |q0| as bits (0: always divide exactly)
+    uint32_t nkeep, omask;
+    int op;                         // its column in XO
+};
+__device__ __forceinline__ QuantLane quant_lane(const NormQuantArgs& g, int j0, bool in) {
+    QuantLane q;
+    float r[8];
+    int p[8];
+    bool ok = true;
+    q.omask = 0;
+    q.nkeep = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        q.s[i] = in ? g.s[j0 + i] : 1.0f;
+        r[i] = in ? g.rcp[j0 + i] : 1.0f;
+        p[i] = in ? g.pos[j0 + i] : -1;
+        q.omask |= (p[i] >= 0 ? 1u : 0u) << i;
+        q.nkeep |= (p[i] >= 0 ? 0u : 0xFu) << (4 * i);
+        q.rz[i] = p[i] >= 0 ? 0.0f : r[i];
+        ok &= div_fast_ok_s(q.s[i]);
+    }
+    const int o = q.omask ? __builtin_ctz(q.omask) : 0;
+    q.so = q.s[0]; q.ro = r[0]; q.op = p[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) {
+        q.so = o == i ? q.s[i] : q.so;
+        q.ro = o == i ? r[i] : q.ro;
+        q.op = o == i ? p[i] : q.op;
+    }
+    q.lim = __uint_as_float(ok ? kF32Pow126 : 0u);
+    return q;
+}
+
+// E2M1 codes (packed, first value in the low nibble) and E8M0 code of 8 bf16
+// values w of a row, 4 lanes forming a block of 32, and their outlier values
+// into the row's part xo of XO: the activation quantizer's arithmetic with its
+// conditions for the fast division (k_quant.hip states them), and the
+// correctly rounded division for the wave where a lane fails one.
+__device__ __forceinline__ uint32_t quant8(const NormQuantArgs& g, const QuantLane& L, u32x4 w, int j0, uint8_t* xo,
+                                           uint32_t& code) {
+    float q[8], a0 = 0.0f, aq = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t wi = w[i >> 1];
+        const float x = __uint_as_float((i & 1) ? (wi & 0xFFFF0000u) : (wi << 16));
+        const float q0 = x * L.rz[i];
+        const float t = __builtin_fmaf(q0, L.s[i], -x);
+        q[i] = __builtin_fmaf(-t, L.rz[i], q0);
+        a0 = fmaxf(a0, __builtin_fabsf(q0));
+        aq = fmaxf(aq, __builtin_fabsf(q[i]));
+    }
+    uint32_t qb = quad_max_bits(__float_as_uint(aq));
+    uint64_t bad = __builtin_amdgcn_uicmp(__float_as_uint(a0), __float_as_uint(L.lim), kCmpUGE) |
+                   __builtin_amdgcn_uicmp(qb - 1u, kF32PowM74 - 1u, kCmpULT);
+    const int o = L.omask ? __builtin_ctz(L.omask) : 0;
+    float vo = 0.0f, qo = 0.0f;
+    const bool any = __builtin_amdgcn_ballot_w64(L.omask != 0) != 0;
+    if (any) {
+        uint32_t wo = w[0];
+#pragma unroll
+        for (int i = 1; i < 4; ++i) wo = (o >> 1) == i ? w[i] : wo;
+        vo = __uint_as_float((o & 1) ? (wo & 0xFFFF0000u) : (wo << 16));
+        qo = div_fast(vo, L.so, L.ro);
+        const uint32_t ab = __float_as_uint(qo) & 0x7FFFFFFFu;
+        bad |= __builtin_amdgcn_uicmp(L.omask ? ab - kF32PowM78 : 0u, kF32Pow126 - kF32PowM78, kCmpUGE) &
+               __builtin_amdgcn_uicmp(ab, 0u, kCmpNE);
+    }
+    if (bad) {
+        aq = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const uint32_t wi = w[i >> 1];
+            const float x = (L.omask >> i) & 1u ? 0.0f : __uint_as_float((i & 1) ? (wi & 0xFFFF0000u) : (wi << 16));
+            q[i] = __fdiv_rn(x, L.s[i]);
+            aq = fmaxf(aq, __builtin_fabsf(q[i]));
+        }
+        qb = quad_max_bits(__float_as_uint(aq));
+        if (any) qo = __fdiv_rn(vo, L.so);
+    }
+    if (any) {
+        auto column = [](int p) { return (p >> 4) * kFragBlock + ((p >> 3) & 1) * 512 + 2 * (p & 7); };
+        if (L.omask) *reinterpret_cast<uint16_t*>(xo + column(L.op)) = (uint16_t)f32_to_bf16_rne(qo);
+        for (uint32_t mm = L.omask & (L.omask - 1); mm; mm &= mm - 1) {      // further ones of the thread
+            const int i = __builtin_ctz(mm);
+            uint32_t wi = w[0];
+#pragma unroll
+            for (int c = 1; c < 4; ++c) wi = (i >> 1) == c ? w[c] : wi;
+            const float x = __uint_as_float((i & 1) ? (wi & 0xFFFF0000u) : (wi << 16));
+            *reinterpret_cast<uint16_t*>(xo + column(g.pos[j0 + i])) = (uint16_t)f32_to_bf16_rne(__fdiv_rn(x, g.s[j0 + i]));
+        }
+    }
+    const int32_t sb = __builtin_elementwise_max((int32_t)(qb & 0x7F800000u) - (2 << 23), 0x00200000);
+    const float scale = __int_as_float(sb);
+    code = (uint32_t)sb >> 23;
+    uint32_t word = 0;
+    MG_CVT_FP4X2(word, q[0], q[1], scale, 0);
+    MG_CVT_FP4X2(word, q[2], q[3], scale, 1);
+    MG_CVT_FP4X2(word, q[4], q[5], scale, 2);
+    MG_CVT_FP4X2(word, q[6], q[7], scale, 3);
+    return word & L.nkeep;
+}
+
+// Norm, modulation, rounding to bf16 and the quantize step.  A workgroup takes
+// units of R consecutive rows (8 where there are enough: whole 128-byte lines
+// of the operand's fragment blocks and scale windows).  Each row's codes are
+// staged in LDS and a unit's rows leave together.  Rows are row_kernel's, with
+// the same sums, so the codes are those of its bf16 output quantized.
+template <int V, typename XT>
+__global__ void __launch_bounds__(V <= 4 ? 512 : 1024) __attribute__((amdgpu_waves_per_eu(V > 4 ? 4 : V == 4 ? 2 : V == 2 ? 2 : 4)))
+norm_quant_kernel(NormQuantArgs g, int R) {
+    constexpr bool KEEP = V <= 4;
+    __shared__ Pairs pairs;
+    extern __shared__ __attribute__((aligned(16))) uint8_t stage[];   // R rows: codes (256 bytes a window, 16 pad), scales (16)
     int turn = 0;
     const RowArgs& a = g.r;
-    const int K = a.K;
+    const int K = a.K, nwin = (int)sc_nwin(K), tid = threadIdx.x;
     const RowThread<V> t(K);
+    const XT* X = static_cast<const XT*>(a.X);
     const int64_t ns4 = frag_slices(K / 2), nso = frag_slices(2 * (int64_t)g.k);
-    const int64_t Mp = (a.M + kScRows - 1) / kScRows * kScRows, M32 = (a.M + 31) / 32 * 32;
-    for (int64_t r = blockIdx.x; r < Mp; r += gridDim.x) {
-        const bool live = r < a.M, piece = r < M32;
-        float x[V][8] = {};
-        if (live) {
-            const int mi = mod_row(a.mod, r);
+    const int64_t M = a.M, M32 = (M + 31) / 32 * 32, Mp = (M + kScRows - 1) / kScRows * kScRows;
+    const int rowA = nwin * 256 + 16, rowS = nwin * 16;
+    uint8_t* const stS = stage + (size_t)R * rowA;
+    float na[KEEP ? V : 1][8], nc[KEEP ? V : 1][8];
+    QuantLane ql[KEEP ? V : 1];
+    int mi_of = -1, mrow = -1;
+    if constexpr (KEEP) {
 #pragma unroll
-            for (int v = 0; v < V; ++v) load8(a.X, r * a.ldx + t.col[v], a.x_dtype, t.left(v), x[v]);
+        for (int v = 0; v < V; ++v) ql[v] = quant_lane(g, t.col[v], t.col[v] < K);
+    }
+    Raw8<XT> rx[V];
+    auto load_row = [&](int64_t r) {
+        r = r < M ? r : M - 1;
+#pragma unroll
+        for (int v = 0; v < V; ++v) load_raw(X + r * a.ldx + t.at[v], rx[v]);
+        mrow = mod_row(a.mod, r);
+    };
+    const int64_t step = (int64_t)gridDim.x * R;
+    int64_t r0 = (int64_t)blockIdx.x * R;
+    if (KEEP) load_row(r0);
+    for (; r0 < Mp; r0 += step) {
+        const int live = r0 >= M ? 0 : M - r0 < R ? (int)(M - r0) : R;
+        for (int rr = 0; rr < live; ++rr) {
+            const int64_t r = r0 + rr;
+            if constexpr (!KEEP) load_row(r);
+            const int mi = __builtin_amdgcn_readfirstlane(mrow);
+            if (KEEP && mi >= 0 && mi != mi_of) {
+#pragma unroll
+                for (int v = 0; v < V; ++v) fold8(t, a.norm, a.mod, mi, v, na[v], nc[v]);
+                mi_of = mi;
+            }
+            float x[V][8];
+#pragma unroll
+            for (int v = 0; v < V; ++v) unpack(rx[v], x[v]);
+            if constexpr (KEEP) load_row(rr + 1 < live ? r + 1 : r0 + step);
             float mean, rstd;
-            row_stats<V>(x, t, a.norm, pair, turn, mean, rstd);
+            row_stats<V>(x, t, a.norm.kind, a.norm.eps, pairs, turn, mean, rstd);
+            uint8_t* const xo = g.XO + (r >> 5) * nso * kFragBlock + ((r & 31) << 4);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                norm8(x[v], t.col[v], t.left(v), a.norm, mean, rstd);
-                mod8(x[v], t.col[v], t.left(v), a.mod, mi);
-            }
-        }
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int j0 = t.col[v];
-            if (j0 >= (K + 511) / 512 * 512) continue;        // whole waves
-            float q[8], amax = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                q[i] = 0.0f;
-                if (j0 < K) {                                 // K % 32 == 0: whole vectors
-                    q[i] = __fdiv_rn(bf16_to_f32(pack_bf16(x[v][i], 0.0f) & 0xFFFFu), g.s[j0 + i]);
-                    const int p = g.pos[j0 + i];
-                    if (p >= 0) {
-                        if (piece)
-                            *reinterpret_cast<uint16_t*>(g.XO + frag_offset(r, 2 * (int64_t)p, nso)) =
-                                (uint16_t)f32_to_bf16_rne(q[i]);
-                        q[i] = 0.0f;
-                    }
+                const int win = v * t.W + t.wave;
+                if (win >= nwin) continue;                            // whole waves
+                if constexpr (!KEEP) {
+                    fold8(t, a.norm, a.mod, mi < 0 ? 0 : mi, v, na[0], nc[0]);
+                    ql[0] = quant_lane(g, t.col[v], t.col[v] < K);
                 }
-                amax = fmaxf(amax, __builtin_fabsf(q[i]));
+                apply8(x[v], mean, rstd, na[KEEP ? v : 0], nc[KEEP ? v : 0]);
+                u32x4 w = pack8_bf16(x[v]);
+                const bool on = mi >= 0 && t.col[v] < K;              // K % 32 == 0: whole blocks
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[i] = on ? w[i] : 0u;
+                uint32_t code;
+                const uint32_t word = quant8(g, ql[KEEP ? v : 0], w, t.col[v], xo, code);
+                const int l = tid & 63;
+                *reinterpret_cast<uint32_t*>(stage + rr * rowA + win * 256 + 4 * l) = word;
+                if ((l & 3) == 0) stS[rr * rowS + win * 16 + sc_pos(l >> 2)] = (uint8_t)code;
             }
-            const uint32_t c = e8m0_from_amax_bits(quad_max_bits(__float_as_uint(amax)));
-            const float scale = e8m0_to_f32(c);
-            uint32_t word = 0;
-            MG_CVT_FP4X2(word, q[0], q[1], scale, 0);
-            MG_CVT_FP4X2(word, q[2], q[3], scale, 1);
-            MG_CVT_FP4X2(word, q[4], q[5], scale, 2);
-            MG_CVT_FP4X2(word, q[6], q[7], scale, 3);
-            if (piece && j0 < 64 * ns4) *reinterpret_cast<uint32_t*>(g.Aq + frag_offset(r, j0 / 2, ns4)) = word;
-            if ((threadIdx.x & 3) == 0) g.As[sc_offset(r, j0 / 32, sc_nwin(K))] = (uint8_t)c;
+            if (tid < 16 * (int)nso - g.k) {                          // pad columns of XO
+                const int p = g.k + tid;
+                *reinterpret_cast<uint16_t*>(xo + (p >> 4) * kFragBlock + ((p >> 3) & 1) * 512 + 2 * (p & 7)) = 0;
+            }
         }
-        if (piece && (int)threadIdx.x < 16 * (int)nso - g.k)
-            *reinterpret_cast<uint16_t*>(g.XO + frag_offset(r, 2 * (int64_t)(g.k + threadIdx.x), nso)) = 0;
+        if (live) __syncthreads();                                    // the unit's codes are staged
+        const int T = t.T, rows = M32 - r0 < R ? (M32 > r0 ? (int)(M32 - r0) : 0) : R;
+        const u32x4 zero = {0, 0, 0, 0};
+        // 16-byte pieces, rows fastest: R of them are contiguous in memory
+        uint8_t* const aq = g.Aq + (r0 >> 5) * ns4 * kFragBlock + ((r0 & 31) << 4);
+        for (int i = tid; i < (int)ns4 * 2 * R; i += T) {
+            const int rr = i & (R - 1), line = i / R;
+            if (rr < rows)
+                *reinterpret_cast<u32x4*>(aq + (line >> 1) * kFragBlock + (line & 1) * 512 + rr * 16) =
+                    rr < live ? *reinterpret_cast<const u32x4*>(stage + rr * rowA + line * 16) : zero;
+        }
+        uint8_t* const as = g.As + (r0 / kScRows) * nwin * kScWinBytes + (r0 % kScRows) * kScBlocks;
+        for (int i = tid; i < nwin * R; i += T) {
+            const int rr = i & (R - 1), win = i / R;
+            *reinterpret_cast<u32x4*>(as + (int64_t)win * kScWinBytes + rr * kScBlocks) =
+                rr < live ? *reinterpret_cast<const u32x4*>(stS + rr * rowS + win * 16) : zero;
+        }
+        if (live < rows) {                                            // pad rows of XO
+            uint8_t* const xo = g.XO + (r0 >> 5) * nso * kFragBlock + ((r0 & 31) << 4);
+            for (int i = tid; i < (int)nso * 2 * R; i += T) {
+                const int rr = i & (R - 1), line = i / R;
+                if (rr >= live && rr < rows)
+                    *reinterpret_cast<u32x4*>(xo + (line >> 1) * kFragBlock + (line & 1) * 512 + rr * 16) = zero;
+            }
+        }
     }
 }
 
@@ -322,8 +681,7 @@ __global__ void __launch_bounds__(64 * kMaxWaves) norm_quant_kernel(NormQuantArg
 struct Shape { int W, V; };
 Shape shape_of(int32_t K) {
     const int nw = (K + 511) / 512;
-    int V = (nw + 7) / 8;
-    V = V <= 4 ? V : 8;
+    const int need = (nw + 7) / 8, V = need <= 2 ? need : need <= 4 ? 4 : 8;
     return Shape{(nw + V - 1) / V, V};
 }
 
@@ -332,30 +690,85 @@ hipError_t by_v(int V, F&& f) {
     switch (V) {
         case 1: return f(std::integral_constant<int, 1>{});
         case 2: return f(std::integral_constant<int, 2>{});
-        case 3: return f(std::integral_constant<int, 3>{});
         case 4: return f(std::integral_constant<int, 4>{});
         default: return f(std::integral_constant<int, 8>{});
     }
 }
 
+// Workgroups of `threads` threads and `lds` bytes of a kernel that run on the
+// device at once, looked up once per device, kernel and size.
+int64_t resident(const void* kern, int threads, int lds) {
+    struct Entry { const void* k; int threads, lds, dev, n; };
+    static thread_local Entry cache[64] = {};
+    static thread_local int used = 0;
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess) return device_cu_count();
+    for (int i = 0; i < used; ++i)
+        if (cache[i].k == kern && cache[i].threads == threads && cache[i].lds == lds && cache[i].dev == dev) return cache[i].n;
+    int n = 0;
+    if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, lds) != hipSuccess || n < 1) n = 1;
+    n *= device_cu_count();
+    if (used < 64) cache[used++] = Entry{kern, threads, lds, dev, n};
+    return n;
+}
+
+template <int V, typename XT, typename YT>
+hipError_t run_rows(const RowArgs& a, int W, hipStream_t st) {
+    const auto kern = row_kernel<V, XT, YT>;
+    const int64_t most = resident(reinterpret_cast<const void*>(kern), 64 * W, 0);
+    const bool same = !a.mod.index && !a.gate.index && (int64_t)a.mod.group >= a.M && (int64_t)a.gate.group >= a.M;
+    const int64_t chunk = (a.M + most - 1) / most;
+    const int64_t blocks = same ? (a.M < most ? a.M : most) : (a.M + chunk - 1) / chunk;
+    hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(64 * W), 0, st, a, RowSpan{chunk, same ? blocks : 1});
+    return hipGetLastError();
+}
+
+template <int V, typename XT>
+hipError_t run_quant(const NormQuantArgs& a, int W, hipStream_t st) {
+    const auto kern = norm_quant_kernel<V, XT>;
+    const int nwin = (int)sc_nwin(a.r.K), row = nwin * 272 + 16;       // staged bytes of a row
+    // 8 rows a unit where that leaves every CU a unit, fewer for few rows
+    int R = 8;
+    while (R > 1 && ((a.r.M + R - 1) / R < device_cu_count() || R * row > 128 * 1024)) R >>= 1;
+    const int lds = R * row;
+    static thread_local int configured_dev = -1;
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess) return hipErrorNoDevice;
+    if (configured_dev != dev) {
+        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern),
+                                                 hipFuncAttributeMaxDynamicSharedMemorySize, 128 * 1024);
+        if (e != hipSuccess) return e;
+        configured_dev = dev;
+    }
+    const int64_t most = resident(reinterpret_cast<const void*>(kern), 64 * W, lds);
+    const int64_t units = (a.r.M + kScRows - 1) / kScRows * kScRows / R;
+    hipLaunchKernelGGL(kern, dim3((unsigned)(units < most ? units : most)), dim3(64 * W), lds, st, a, R);
+    return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_rows(const RowArgs& a, hipStream_t st) {
-    const Shape sh = shape_of(a.K);
-    const int64_t blocks = a.M < 65536 ? a.M : 65536;
-    return by_v(sh.V, [&](auto v) {
-        hipLaunchKernelGGL((row_kernel<decltype(v)::value>), dim3((unsigned)blocks), dim3(64 * sh.W), 0, st, a);
+    if (a.K < 8) {
+        hipLaunchKernelGGL(row_small_kernel, dim3((unsigned)((a.M + 255) / 256)), dim3(256), 0, st, a);
         return hipGetLastError();
+    }
+    const Shape sh = shape_of(a.K);
+    return by_v(sh.V, [&](auto v) {
+        constexpr int V = decltype(v)::value;
+        const bool xf = a.x_dtype == MG_F32, yf = a.y_dtype == MG_F32;
+        if (a.Y == nullptr)
+            return xf ? run_rows<V, float, void>(a, sh.W, st) : run_rows<V, uint16_t, void>(a, sh.W, st);
+        if (xf) return yf ? run_rows<V, float, float>(a, sh.W, st) : run_rows<V, float, uint16_t>(a, sh.W, st);
+        return yf ? run_rows<V, uint16_t, float>(a, sh.W, st) : run_rows<V, uint16_t, uint16_t>(a, sh.W, st);
     });
 }
 
 hipError_t launch_norm_quant(const NormQuantArgs& a, hipStream_t st) {
     const Shape sh = shape_of(a.r.K);
-    const int64_t Mp = (a.r.M + kScRows - 1) / kScRows * kScRows;
-    const int64_t blocks = Mp < 65536 ? Mp : 65536;
     return by_v(sh.V, [&](auto v) {
-        hipLaunchKernelGGL((norm_quant_kernel<decltype(v)::value>), dim3((unsigned)blocks), dim3(64 * sh.W), 0, st, a);
-        return hipGetLastError();
+        constexpr int V = decltype(v)::value;
+        return a.r.x_dtype == MG_F32 ? run_quant<V, float>(a, sh.W, st) : run_quant<V, uint16_t>(a, sh.W, st);
     });
 }
 
