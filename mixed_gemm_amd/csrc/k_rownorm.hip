@@ -79,8 +79,9 @@ __device__ __forceinline__ u32x4 pack8_bf16(const float (&v)[8]) {
     return u32x4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7])};
 }
 
-// A thread's place in rows of K >= 8 channels: V vectors, W waves.
-template <int V>
+// A thread's place in rows of K >= 8 channels: V vectors, W waves.  ODD: K need
+// not be a multiple of 8.
+template <int V, bool ODD = true>
 struct RowThread {
     int W, T, wave, K, shift;       // shift: channels missing in the row's last vector
     int col[V];                     // first channel of vector v
@@ -123,7 +124,7 @@ struct RowThread {
     // Values loaded at at[v] moved to the vector's own channels (those past the
     // row hold anything: they are counted nowhere and never stored).
     __device__ __forceinline__ void place(int v, float (&x)[8]) const {
-        if (cut >> v & 1u) {
+        if (ODD && (cut >> v & 1u)) {
             const bool me = col[v] < K && col[v] > K - 8;
             for (int k = 0; k < shift; ++k) {
 #pragma unroll
@@ -191,8 +192,8 @@ __device__ __forceinline__ float rsqrt_f32(float v) {
 
 // mean (0 for rms) and 1 / sqrt(var + eps) of the row x: the parallel variance
 // formula over the waves, whose pairs the 16 lanes of a row take one each.
-template <int V>
-__device__ __forceinline__ void row_stats(const float (&x)[V][8], const RowThread<V>& t, int kind, float eps, Pairs& pairs,
+template <int V, bool ODD>
+__device__ __forceinline__ void row_stats(const float (&x)[V][8], const RowThread<V, ODD>& t, int kind, float eps, Pairs& pairs,
                                           int& turn, float& mean, float& rstd) {
     float s = 0.0f, m = 0.0f, q = 0.0f;
     const bool layer = kind == MG_NORM_LAYER;
@@ -244,8 +245,8 @@ __device__ __forceinline__ void row_stats(const float (&x)[V][8], const RowThrea
 
 // A norm with its modulation folded to n a + c, n = (x - mean) rstd: a = w (1 +
 // scale_i), c = b (1 + scale_i) + shift_i of 8 channels.
-template <int V>
-__device__ __forceinline__ void fold8(const RowThread<V>& t, const NormArgs& n, const ModArgs& m, int row, int v,
+template <int V, bool ODD>
+__device__ __forceinline__ void fold8(const RowThread<V, ODD>& t, const NormArgs& n, const ModArgs& m, int row, int v,
                                       float (&a)[8], float (&c)[8]) {
     float w[8];
 #pragma unroll
@@ -376,7 +377,7 @@ row_kernel(RowArgs a, RowSpan span) {
         if constexpr (S::ahead) load_row(next <= last ? next : last);
         if constexpr (RES) {
             float mean = 0.0f, rstd = 1.0f;
-            if (a.has_post) row_stats<V>(y, t, a.post.kind, a.post.eps, pairs, turn, mean, rstd);
+            if (a.has_post) row_stats(y, t, a.post.kind, a.post.eps, pairs, turn, mean, rstd);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 if (gi >= 0) {
@@ -393,7 +394,7 @@ row_kernel(RowArgs a, RowSpan span) {
         }
         if (!RES || a.has_norm) {
             float mean, rstd;
-            row_stats<V>(x, t, a.norm.kind, a.norm.eps, pairs, turn, mean, rstd);
+            row_stats(x, t, a.norm.kind, a.norm.eps, pairs, turn, mean, rstd);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 if (mi >= 0) {
@@ -502,11 +503,11 @@ __device__ __forceinline__ QuantLane quant_lane(const NormQuantArgs& g, int j0, 
 
 // E2M1 codes (packed, first value in the low nibble) and E8M0 code of 8 bf16
 // values w of a row, 4 lanes forming a block of 32, and their outlier values
-// into the row's part xo of XO: the activation quantizer's arithmetic with its
+// into the row's part xo of XO (any: a lane of the wave has one): the activation quantizer's arithmetic with its
 // conditions for the fast division (k_quant.hip states them), and the
 // correctly rounded division for the wave where a lane fails one.
 __device__ __forceinline__ uint32_t quant8(const NormQuantArgs& g, const QuantLane& L, u32x4 w, int j0, uint8_t* xo,
-                                           uint32_t& code) {
+                                           uint32_t& code, bool any) {
     float q[8], a0 = 0.0f, aq = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -523,7 +524,6 @@ __device__ __forceinline__ uint32_t quant8(const NormQuantArgs& g, const QuantLa
                    __builtin_amdgcn_uicmp(qb - 1u, kF32PowM74 - 1u, kCmpULT);
     const int o = L.omask ? __builtin_ctz(L.omask) : 0;
     float vo = 0.0f, qo = 0.0f;
-    const bool any = __builtin_amdgcn_ballot_w64(L.omask != 0) != 0;
     if (any) {
         uint32_t wo = w[0];
 #pragma unroll
@@ -569,13 +569,75 @@ __device__ __forceinline__ uint32_t quant8(const NormQuantArgs& g, const QuantLa
     return word & L.nkeep;
 }
 
+// The norm's and the modulation's arguments, read from the kernel-argument
+// segment (whose start is the kernel's first parameter) where they are used,
+// through a pointer the compiler cannot see through: held in scalar registers
+// across the rows they would be spilled there.
+struct FoldArgs {
+    NormArgs norm;
+    ModArgs mod;
+};
+__device__ __forceinline__ FoldArgs fold_args() {
+    typedef const __attribute__((address_space(4))) NormQuantArgs* KernargPtr;
+    KernargPtr p = (KernargPtr)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    FoldArgs f;
+    f.norm.weight = p->r.norm.weight;
+    f.norm.bias = p->r.norm.bias;
+    f.norm.dtype = p->r.norm.dtype;
+    f.norm.kind = p->r.norm.kind;
+    f.norm.eps = p->r.norm.eps;
+    f.mod.scale = p->r.mod.scale;
+    f.mod.shift = p->r.mod.shift;
+    f.mod.gate = nullptr;
+    f.mod.index = nullptr;
+    f.mod.ld = p->r.mod.ld;
+    f.mod.group = 1;
+    f.mod.rows = p->r.mod.rows;
+    f.mod.dtype = p->r.mod.dtype;
+    return f;
+}
+
+// A unit's rows r0 ... r0 + R - 1 from their staged codes (`live` of them; zeros
+// for pad rows) to Aq and As, and the pad rows of XO, by T threads: 16-byte
+// pieces, rows fastest, R of them contiguous in memory.
+template <int FIXED>
+__device__ __forceinline__ void flush_unit(const NormQuantArgs& g, int64_t r0, int live, int64_t M32, int64_t ns4, int64_t nso,
+                                           int nwin, const uint8_t* stA, int rowA, const uint8_t* stS, int rowS, int T,
+                                           int R_ = FIXED) {
+    const int R = FIXED ? FIXED : R_, tid = threadIdx.x;
+    const int rows = M32 - r0 < R ? (M32 > r0 ? (int)(M32 - r0) : 0) : R;
+    const u32x4 zero = {0, 0, 0, 0};
+    uint8_t* const aq = g.Aq + (r0 >> 5) * ns4 * kFragBlock + ((r0 & 31) << 4);
+    for (int i = tid; i < (int)ns4 * 2 * R; i += T) {
+        const int rr = i & (R - 1), line = i / R;
+        if (rr < rows)
+            *reinterpret_cast<u32x4*>(aq + (line >> 1) * kFragBlock + (line & 1) * 512 + rr * 16) =
+                rr < live ? *reinterpret_cast<const u32x4*>(stA + rr * rowA + line * 16) : zero;
+    }
+    uint8_t* const as = g.As + (r0 / kScRows) * nwin * kScWinBytes + (r0 % kScRows) * kScBlocks;
+    for (int i = tid; i < nwin * R; i += T) {
+        const int rr = i & (R - 1), win = i / R;
+        *reinterpret_cast<u32x4*>(as + (int64_t)win * kScWinBytes + rr * kScBlocks) =
+            rr < live ? *reinterpret_cast<const u32x4*>(stS + rr * rowS + win * 16) : zero;
+    }
+    if (live < rows) {
+        uint8_t* const xo = g.XO + (r0 >> 5) * nso * kFragBlock + ((r0 & 31) << 4);
+        for (int i = tid; i < (int)nso * 2 * R; i += T) {
+            const int rr = i & (R - 1), line = i / R;
+            if (rr >= live && rr < rows)
+                *reinterpret_cast<u32x4*>(xo + (line >> 1) * kFragBlock + (line & 1) * 512 + rr * 16) = zero;
+        }
+    }
+}
+
 // Norm, modulation, rounding to bf16 and the quantize step.  A workgroup takes
 // units of R consecutive rows (8 where there are enough: whole 128-byte lines
 // of the operand's fragment blocks and scale windows).  Each row's codes are
 // staged in LDS and a unit's rows leave together.  Rows are row_kernel's, with
 // the same sums, so the codes are those of its bf16 output quantized.
 template <int V, typename XT>
-__global__ void __launch_bounds__(V <= 4 ? 512 : 1024) __attribute__((amdgpu_waves_per_eu(V > 4 ? 4 : V == 4 ? 2 : V == 2 ? 2 : 4)))
+__global__ void __launch_bounds__(V <= 4 ? 512 : 1024) __attribute__((amdgpu_waves_per_eu(V > 4 ? 4 : V == 4 ? 2 : V == 2 ? 3 : 4)))
 norm_quant_kernel(NormQuantArgs g, int R) {
     constexpr bool KEEP = V <= 4;
     __shared__ Pairs pairs;
@@ -583,7 +645,7 @@ norm_quant_kernel(NormQuantArgs g, int R) {
     int turn = 0;
     const RowArgs& a = g.r;
     const int K = a.K, nwin = (int)sc_nwin(K), tid = threadIdx.x;
-    const RowThread<V> t(K);
+    const RowThread<V, false> t(K);
     const XT* X = static_cast<const XT*>(a.X);
     const int64_t ns4 = frag_slices(K / 2), nso = frag_slices(2 * (int64_t)g.k);
     const int64_t M = a.M, M32 = (M + 31) / 32 * 32, Mp = (M + kScRows - 1) / kScRows * kScRows;
@@ -613,8 +675,9 @@ norm_quant_kernel(NormQuantArgs g, int R) {
             if constexpr (!KEEP) load_row(r);
             const int mi = __builtin_amdgcn_readfirstlane(mrow);
             if (KEEP && mi >= 0 && mi != mi_of) {
+                const FoldArgs f = fold_args();
 #pragma unroll
-                for (int v = 0; v < V; ++v) fold8(t, a.norm, a.mod, mi, v, na[v], nc[v]);
+                for (int v = 0; v < V; ++v) fold8(t, f.norm, f.mod, mi, v, na[v], nc[v]);
                 mi_of = mi;
             }
             float x[V][8];
@@ -622,14 +685,15 @@ norm_quant_kernel(NormQuantArgs g, int R) {
             for (int v = 0; v < V; ++v) unpack(rx[v], x[v]);
             if constexpr (KEEP) load_row(rr + 1 < live ? r + 1 : r0 + step);
             float mean, rstd;
-            row_stats<V>(x, t, a.norm.kind, a.norm.eps, pairs, turn, mean, rstd);
+            row_stats(x, t, a.norm.kind, a.norm.eps, pairs, turn, mean, rstd);
             uint8_t* const xo = g.XO + (r >> 5) * nso * kFragBlock + ((r & 31) << 4);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const int win = v * t.W + t.wave;
                 if (win >= nwin) continue;                            // whole waves
                 if constexpr (!KEEP) {
-                    fold8(t, a.norm, a.mod, mi < 0 ? 0 : mi, v, na[0], nc[0]);
+                    const FoldArgs f = fold_args();
+                    fold8(t, f.norm, f.mod, mi < 0 ? 0 : mi, v, na[0], nc[0]);
                     ql[0] = quant_lane(g, t.col[v], t.col[v] < K);
                 }
                 apply8(x[v], mean, rstd, na[KEEP ? v : 0], nc[KEEP ? v : 0]);
@@ -638,7 +702,8 @@ norm_quant_kernel(NormQuantArgs g, int R) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) w[i] = on ? w[i] : 0u;
                 uint32_t code;
-                const uint32_t word = quant8(g, ql[KEEP ? v : 0], w, t.col[v], xo, code);
+                const QuantLane& L = ql[KEEP ? v : 0];
+                const uint32_t word = quant8(g, L, w, t.col[v], xo, code, __builtin_amdgcn_ballot_w64(L.omask != 0) != 0);
                 const int l = tid & 63;
                 *reinterpret_cast<uint32_t*>(stage + rr * rowA + win * 256 + 4 * l) = word;
                 if ((l & 3) == 0) stS[rr * rowS + win * 16 + sc_pos(l >> 2)] = (uint8_t)code;
@@ -649,30 +714,206 @@ norm_quant_kernel(NormQuantArgs g, int R) {
             }
         }
         if (live) __syncthreads();                                    // the unit's codes are staged
-        const int T = t.T, rows = M32 - r0 < R ? (M32 > r0 ? (int)(M32 - r0) : 0) : R;
-        const u32x4 zero = {0, 0, 0, 0};
-        // 16-byte pieces, rows fastest: R of them are contiguous in memory
-        uint8_t* const aq = g.Aq + (r0 >> 5) * ns4 * kFragBlock + ((r0 & 31) << 4);
-        for (int i = tid; i < (int)ns4 * 2 * R; i += T) {
-            const int rr = i & (R - 1), line = i / R;
-            if (rr < rows)
-                *reinterpret_cast<u32x4*>(aq + (line >> 1) * kFragBlock + (line & 1) * 512 + rr * 16) =
-                    rr < live ? *reinterpret_cast<const u32x4*>(stage + rr * rowA + line * 16) : zero;
+        flush_unit<0>(g, r0, live, M32, ns4, nso, nwin, stage, rowA, stS, rowS, t.T, R);
+    }
+}
+
+
+// The same with a row per wave, for up to 5120 channels and many rows: the
+// per-channel constants (a, c, s, 1 / s: 16 bytes a channel, and the outlier
+// routing) lie in LDS, once for the 8 waves of the workgroup, a row needs no
+// barrier and one wave's bookkeeping instead of W waves', and its registers
+// are refilled window by window with the next row.  V: windows of 512 channels.
+// The sums are row_kernel's (those of its W waves, one after the other), so
+// the bits are.
+template <int V>
+struct WaveShape {
+    static constexpr int W = V <= 8 ? V : (V + 1) / 2;             // row_kernel's waves (and one or two vectors) for V windows
+    static constexpr int rowA = V * 256 + 16, rowS = V * 16;       // staged bytes of a row: codes, scales
+    static constexpr int lds = V * 64 * 144 + 2 * 8 * (rowA + rowS);
+};
+template <int V, typename XT>
+__global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) norm_quant_wave_kernel(NormQuantArgs g) {
+    using S = WaveShape<V>;
+    extern __shared__ __attribute__((aligned(16))) uint8_t stage[];
+    float4* const ka = reinterpret_cast<float4*>(stage);            // a, c, s, rz: [array][window][half][lane]
+    uint4* const ko = reinterpret_cast<uint4*>(stage + V * 64 * 128);  // nkeep, XO column, s and 1 / s of the first outlier
+    uint8_t* const st = stage + V * 64 * 144;
+    const RowArgs& a = g.r;
+    const int K = a.K, nwin = (int)sc_nwin(K), tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const XT* X = static_cast<const XT*>(a.X);
+    const int64_t ns4 = frag_slices(K / 2), nso = frag_slices(2 * (int64_t)g.k);
+    const int64_t M = a.M, M32 = (M + 31) / 32 * 32, Mp = (M + kScRows - 1) / kScRows * kScRows;
+    auto slot = [&](int arr, int win, int half, int l) -> float4& { return ka[((arr * V + win) * 2 + half) * 64 + l]; };
+    auto put8 = [&](int arr, int win, int l, const float (&v)[8]) {
+        slot(arr, win, 0, l) = make_float4(v[0], v[1], v[2], v[3]);
+        slot(arr, win, 1, l) = make_float4(v[4], v[5], v[6], v[7]);
+    };
+    auto get8 = [&](int arr, int win, float (&v)[8]) {
+        const float4 x = slot(arr, win, 0, lane), y = slot(arr, win, 1, lane);
+        v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w; v[4] = y.x; v[5] = y.y; v[6] = y.z; v[7] = y.w;
+    };
+    // a thread's place as fold8 needs it: one vector at a time
+    RowThread<1, false> t(K);
+    auto at_window = [&](int win, int l) {
+        t.col[0] = (win * 64 + l) * 8;
+        t.at[0] = t.col[0] < K - 8 ? t.col[0] : K - 8;
+    };
+    for (int i = tid; i < V * 64; i += 512) {
+        const int win = i >> 6, l = i & 63, j0 = i * 8;
+        const QuantLane q = quant_lane(g, j0, j0 < K);
+        put8(2, win, l, q.s);
+        put8(3, win, l, q.rz);
+        ko[i] = make_uint4(q.nkeep, (uint32_t)q.op, __float_as_uint(q.so), __float_as_uint(q.ro));
+    }
+    __syncthreads();
+    uint32_t outl = 0, slow = 0;        // windows with an outlier channel; whose s is out of the fast division's range
+    for (int win = 0; win < V; ++win) {
+        float s[8];
+        get8(2, win, s);
+        bool ok = true;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ok &= div_fast_ok_s(s[i]);
+        outl |= (__builtin_amdgcn_ballot_w64(ko[win * 64 + lane].x != 0xFFFFFFFFu) ? 1u : 0u) << win;
+        slow |= (__builtin_amdgcn_ballot_w64(!ok) ? 1u : 0u) << win;
+    }
+    // channels of row_kernel's waves: the lane's (lane % 16), and its own share of each
+    float nl, rnl;
+    {
+        int c = 0;
+        for (int v = 0; v * S::W < V; ++v) {
+            const int l = K - 512 * (v * S::W + (lane & 15));
+            c += (lane & 15) >= S::W || l < 0 ? 0 : l < 512 ? l : 512;
         }
-        uint8_t* const as = g.As + (r0 / kScRows) * nwin * kScWinBytes + (r0 % kScRows) * kScBlocks;
-        for (int i = tid; i < nwin * R; i += T) {
-            const int rr = i & (R - 1), win = i / R;
-            *reinterpret_cast<u32x4*>(as + (int64_t)win * kScWinBytes + rr * kScBlocks) =
-                rr < live ? *reinterpret_cast<const u32x4*>(stS + rr * rowS + win * 16) : zero;
+        nl = (float)c;
+        rnl = c ? 1.0f / (float)c : 0.0f;
+    }
+    const float rK = 1.0f / (float)K;
+    const bool layer = a.norm.kind == MG_NORM_LAYER;
+    const float eps = a.norm.eps;
+    int loaded = -1, turn = 0;
+    Raw8<XT> rx[V];
+    auto load_win = [&](int64_t r, int v) {
+        const int col = 512 * v + 8 * lane;
+        load_raw(X + (r < M ? r : M - 1) * a.ldx + (col < K - 8 ? col : K - 8), rx[v]);
+    };
+    const int64_t step = (int64_t)gridDim.x * 8;
+    int64_t r0 = (int64_t)blockIdx.x * 8;
+#pragma unroll
+    for (int v = 0; v < V; ++v) load_win(r0 + wave, v);
+    auto mod_rows = [&](int64_t r) { return lane < 8 && r + lane < M ? mod_row(a.mod, r + lane) : -1; };
+    int mis = mod_rows(r0);
+    for (; r0 < Mp; r0 += step) {
+        const int64_t r = r0 + wave;
+        const int live = r0 >= M ? 0 : M - r0 < 8 ? (int)(M - r0) : 8;
+        const int mi = __builtin_amdgcn_readlane(mis, wave);
+        const uint64_t some = __builtin_amdgcn_ballot_w64(mis >= 0);
+        const int want = some ? __builtin_amdgcn_readlane(mis, __builtin_ctzll(some)) : loaded;
+        mis = mod_rows(r0 + step);
+        if (want != loaded) {           // the same in every wave
+            __syncthreads();
+            const FoldArgs f = fold_args();
+            for (int i = tid; i < V * 64; i += 512) {
+                float na[8], nc[8];
+                at_window(i >> 6, i & 63);
+                fold8(t, f.norm, f.mod, want, 0, na, nc);
+                put8(0, i >> 6, i & 63, na);
+                put8(1, i >> 6, i & 63, nc);
+            }
+            __syncthreads();
+            loaded = want;
         }
-        if (live < rows) {                                            // pad rows of XO
-            uint8_t* const xo = g.XO + (r0 >> 5) * nso * kFragBlock + ((r0 & 31) << 4);
-            for (int i = tid; i < (int)nso * 2 * R; i += T) {
-                const int rr = i & (R - 1), line = i / R;
-                if (rr >= live && rr < rows)
-                    *reinterpret_cast<u32x4*>(xo + (line >> 1) * kFragBlock + (line & 1) * 512 + rr * 16) = zero;
+        uint8_t* const stA = st + turn * 8 * (S::rowA + S::rowS), * const stS = stA + 8 * S::rowA;
+        if (wave < live) {
+            // the sums of row_kernel's wave w: windows w, w + W
+            float s = 0.0f, q = 0.0f;   // of wave (lane % 16)
+            float x[V][8];
+#pragma unroll
+            for (int v = 0; v < V; ++v) unpack(rx[v], x[v]);
+            auto count = [&](int w) {   // channels of wave w
+                int c = 0;
+#pragma unroll
+                for (int v = 0; v * S::W < V; ++v) {
+                    const int l = K - 512 * (v * S::W + w);
+                    c += l < 0 ? 0 : l < 512 ? l : 512;
+                }
+                return c;
+            };
+#pragma unroll
+            for (int w = 0; w < S::W; ++w) {
+                float sw = 0.0f, qw = 0.0f, m = 0.0f;
+                if (layer) {
+#pragma unroll
+                    for (int v = w; v < V; v += S::W)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) sw += 512 * v + 8 * lane < K ? x[v][i] : 0.0f;
+                    sw = wave_sum(sw);
+                    const int c = count(w);
+                    m = sw * (c ? 1.0f / (float)c : 0.0f);
+                }
+#pragma unroll
+                for (int v = w; v < V; v += S::W)
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const float d = 512 * v + 8 * lane < K ? x[v][i] - m : 0.0f;
+                        qw = __builtin_fmaf(d, d, qw);
+                    }
+                qw = wave_sum(qw);
+                s = (lane & 15) == w ? sw : s;
+                q = (lane & 15) == w ? qw : q;
+            }
+            const float mean = layer ? row16_sum(s) * rK : 0.0f;
+            const float d = s * rnl - mean;
+            const float rstd = rsqrt_f32(__builtin_fmaf(row16_sum(__builtin_fmaf(nl * d, d, q)), rK, eps));
+            uint8_t* const xo = g.XO + (r >> 5) * nso * kFragBlock + ((r & 31) << 4);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const int j0 = 512 * v + 8 * lane;
+                float na[8], nc[8];
+                if (mi == loaded || mi < 0) {
+                    get8(0, v, na);
+                    get8(1, v, nc);
+                } else {
+                    const FoldArgs f = fold_args();
+                    at_window(v, lane);
+                    fold8(t, f.norm, f.mod, mi, 0, na, nc);
+                }
+                apply8(x[v], mean, rstd, na, nc);
+                u32x4 w = pack8_bf16(x[v]);
+                const bool on = mi >= 0 && j0 < K;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[i] = on ? w[i] : 0u;
+                load_win(r + step, v);
+                QuantLane L;
+                get8(2, v, L.s);
+                get8(3, v, L.rz);
+                const uint4 o = ko[v * 64 + lane];
+                L.nkeep = o.x;
+                L.op = (int)o.y;
+                L.so = __uint_as_float(o.z);
+                L.ro = __uint_as_float(o.w);
+                L.omask = 0;
+                if (outl >> v & 1u) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) L.omask |= ((o.x >> (4 * i) & 1u) ^ 1u) << i;
+                }
+                L.lim = __uint_as_float(slow >> v & 1u ? 0u : kF32Pow126);
+                uint32_t code;
+                const uint32_t word = quant8(g, L, w, j0, xo, code, outl >> v & 1u);
+                *reinterpret_cast<uint32_t*>(stA + wave * S::rowA + v * 256 + 4 * lane) = word;
+                if ((lane & 3) == 0) stS[wave * S::rowS + v * 16 + sc_pos(lane >> 2)] = (uint8_t)code;
+            }
+            if (lane < 16 * (int)nso - g.k) {                       // pad columns of XO
+                const int p = g.k + lane;
+                *reinterpret_cast<uint16_t*>(xo + (p >> 4) * kFragBlock + ((p >> 3) & 1) * 512 + 2 * (p & 7)) = 0;
             }
         }
+        // one barrier a unit: the next unit stages into the other half, and is
+        // past its barrier only when every wave has left this one's
+        if (live) __syncthreads();
+        turn ^= 1;
+        flush_unit<8>(g, r0, live, M32, ns4, nso, nwin, stA, S::rowA, stS, S::rowS, 512);
     }
 }
 
@@ -746,6 +987,24 @@ hipError_t run_quant(const NormQuantArgs& a, int W, hipStream_t st) {
     return hipGetLastError();
 }
 
+template <int V, typename XT>
+hipError_t run_quant_wave(const NormQuantArgs& a, hipStream_t st) {
+    const auto kern = norm_quant_wave_kernel<V, XT>;
+    constexpr int lds = WaveShape<V>::lds;
+    static thread_local int configured_dev = -1;
+    int dev = 0;
+    if (hipGetDevice(&dev) != hipSuccess) return hipErrorNoDevice;
+    if (configured_dev != dev) {
+        const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+        if (e != hipSuccess) return e;
+        configured_dev = dev;
+    }
+    const int64_t most = resident(reinterpret_cast<const void*>(kern), 512, lds);
+    const int64_t units = (a.r.M + kScRows - 1) / kScRows * (kScRows / 8);
+    hipLaunchKernelGGL(kern, dim3((unsigned)(units < most ? units : most)), dim3(512), lds, st, a);
+    return hipGetLastError();
+}
+
 }  // namespace
 
 hipError_t launch_rows(const RowArgs& a, hipStream_t st) {
@@ -766,6 +1025,15 @@ hipError_t launch_rows(const RowArgs& a, hipStream_t st) {
 
 hipError_t launch_norm_quant(const NormQuantArgs& a, hipStream_t st) {
     const Shape sh = shape_of(a.r.K);
+    const int nw = (a.r.K + 511) / 512;
+    if (a.r.M >= 8 * (int64_t)device_cu_count() && nw <= 10) {
+        const bool xf = a.r.x_dtype == MG_F32;
+        switch (nw) {
+#define MG_WAVE(V) case V: return xf ? run_quant_wave<V, float>(a, st) : run_quant_wave<V, uint16_t>(a, st)
+            MG_WAVE(1); MG_WAVE(2); MG_WAVE(3); MG_WAVE(4); MG_WAVE(5); MG_WAVE(6); MG_WAVE(7); MG_WAVE(8); MG_WAVE(9); MG_WAVE(10);
+#undef MG_WAVE
+        }
+    }
     return by_v(sh.V, [&](auto v) {
         constexpr int V = decltype(v)::value;
         return a.r.x_dtype == MG_F32 ? run_quant<V, float>(a, sh.W, st) : run_quant<V, uint16_t>(a, sh.W, st);

@@ -277,6 +277,18 @@ QUANT_CASES = [
     (9, 16416, 300, "f32", "layer", None, "sample", "f32", 0),
     (3, 65536, 17, "bf16", "layer", None, "token", "f32", 0),
     (40, 544, 544, "bf16", "layer", None, "sample", "f32", 0),
+    # enough rows for the form with a row per wave, every number of windows
+    (2101, 5120, 64, "f32", "layer", "bf16", "token", "f32", 0),
+    (4099, 4640, 33, "bf16", "rms", None, "sample", "bf16", 8),
+    (2100, 32, 3, "f32", "layer", "f32", "token", "f32", 1),
+    (3333, 1024, 0, "bf16", "layer", None, "token", "bf16", 0),
+    (2050, 1376, 300, "f32", "rms", "f32", "sample", "f32", 3),
+    (2049, 2048, 17, "bf16", "layer", None, "sample", "f32", 0),
+    (2600, 2336, 40, "f32", "layer", None, "sample", "f32", 0),
+    (2300, 2592, 5, "bf16", "layer", "bf16", "token", "f32", 0),
+    (2200, 3104, 64, "f32", "layer", None, "token", "bf16", 0),
+    (2150, 3616, 64, "bf16", "rms", "bf16", "sample", "f32", 0),
+    (2500, 4096, 4096, "bf16", "layer", None, "sample", "f32", 0),
 ]
 
 
@@ -309,10 +321,11 @@ def test_norm_quantize_is_norm_then_quantize(M, K, k, xt, kind, affine, mod, mt,
         assert np.array_equal(x, y), f"{n}: {int((x != y).sum())} of {x.size} bytes differ"
 
 
-def test_norm_quantize_with_scales_out_of_the_fast_range():
+@pytest.mark.parametrize("M", [40, 2100])
+def test_norm_quantize_with_scales_out_of_the_fast_range(M):
     """Smoothing scales far from 1 and rows of tiny values: the exact division's codes."""
     rng = np.random.default_rng(12)
-    M, K, k = 40, 1024, 24
+    K, k = 1024, 24
     X, _ = rows(rng, M, K, "f32")
     X[7] *= 1e-30
     p = _quant_plan(rng, K, 32, k, X.bfloat16())
