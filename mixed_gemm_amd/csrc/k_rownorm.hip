@@ -463,100 +463,69 @@ __global__ void __launch_bounds__(256) row_small_kernel(RowArgs a) {
     }
 }
 
-// Per-thread constants of the quantize step for 8 channels: the smoothing
-// scales s, their reciprocals with 0 on outlier channels (whose bulk quotient
-// is then +-0 and whose codes nkeep clears), and the first outlier channel.
+// ---- norm, modulation and the quantize step of the projection behind them
+
+// A thread's 8 channels' smoothing scales, their reciprocals with 0 on outlier
+// channels (whose bulk quotient is then +-0 and whose codes `keep` clears), and
+// the bound of the fast quotient (0 where a scale is out of its range).
 struct QuantLane {
     float s[8], rz[8];
-    float so, ro, lim;              // the first outlier's s and 1 / s; bound of |q0| as bits (0: always divide exactly)
-    uint32_t nkeep, omask;
-    int op;                         // its column in XO
+    uint32_t keep, lim;
 };
-__device__ __forceinline__ QuantLane quant_lane(const NormQuantArgs& g, int j0, bool in) {
-    QuantLane q;
-    float r[8];
-    int p[8];
+__device__ __forceinline__ void quant_lane(const NormQuantArgs& g, int j0, bool in, QuantLane& q) {
     bool ok = true;
-    q.omask = 0;
-    q.nkeep = 0;
+    q.keep = 0xFFFFFFFFu;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         q.s[i] = in ? g.s[j0 + i] : 1.0f;
-        r[i] = in ? g.rcp[j0 + i] : 1.0f;
-        p[i] = in ? g.pos[j0 + i] : -1;
-        q.omask |= (p[i] >= 0 ? 1u : 0u) << i;
-        q.nkeep |= (p[i] >= 0 ? 0u : 0xFu) << (4 * i);
-        q.rz[i] = p[i] >= 0 ? 0.0f : r[i];
+        const bool out = in && g.pos[j0 + i] >= 0;
+        q.rz[i] = in && !out ? g.rcp[j0 + i] : 0.0f;
+        q.keep &= out ? ~(0xFu << (4 * i)) : 0xFFFFFFFFu;
         ok &= div_fast_ok_s(q.s[i]);
     }
-    const int o = q.omask ? __builtin_ctz(q.omask) : 0;
-    q.so = q.s[0]; q.ro = r[0]; q.op = p[0];
-#pragma unroll
-    for (int i = 1; i < 8; ++i) {
-        q.so = o == i ? q.s[i] : q.so;
-        q.ro = o == i ? r[i] : q.ro;
-        q.op = o == i ? p[i] : q.op;
-    }
-    q.lim = __uint_as_float(ok ? kF32Pow126 : 0u);
-    return q;
+    q.lim = ok ? kF32Pow126 : 0u;
 }
 
 // E2M1 codes (packed, first value in the low nibble) and E8M0 code of 8 bf16
-// values w of a row, 4 lanes forming a block of 32, and their outlier values
-// into the row's part xo of XO (any: a lane of the wave has one): the activation quantizer's arithmetic with its
-// conditions for the fast division (k_quant.hip states them), and the
-// correctly rounded division for the wave where a lane fails one.
-__device__ __forceinline__ uint32_t quant8(const NormQuantArgs& g, const QuantLane& L, u32x4 w, int j0, uint8_t* xo,
-                                           uint32_t& code, bool any) {
+// values w of a row, 4 lanes forming a block of 32: the activation quantizer's
+// arithmetic with its conditions for the fast division (k_quant.hip states
+// them), and the correctly rounded division for the wave where a lane fails.
+__device__ __forceinline__ uint32_t quant8(const float (&s)[8], const float (&rz)[8], uint32_t keep, uint32_t lim, u32x4 w,
+                                           uint32_t& code) {
     float q[8], a0 = 0.0f, aq = 0.0f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const uint32_t wi = w[i >> 1];
         const float x = __uint_as_float((i & 1) ? (wi & 0xFFFF0000u) : (wi << 16));
-        const float q0 = x * L.rz[i];
-        const float t = __builtin_fmaf(q0, L.s[i], -x);
-        q[i] = __builtin_fmaf(-t, L.rz[i], q0);
+        const float q0 = x * rz[i];
+        const float t = __builtin_fmaf(q0, s[i], -x);
+        q[i] = __builtin_fmaf(-t, rz[i], q0);
         a0 = fmaxf(a0, __builtin_fabsf(q0));
         aq = fmaxf(aq, __builtin_fabsf(q[i]));
     }
     uint32_t qb = quad_max_bits(__float_as_uint(aq));
-    uint64_t bad = __builtin_amdgcn_uicmp(__float_as_uint(a0), __float_as_uint(L.lim), kCmpUGE) |
-                   __builtin_amdgcn_uicmp(qb - 1u, kF32PowM74 - 1u, kCmpULT);
-    const int o = L.omask ? __builtin_ctz(L.omask) : 0;
-    float vo = 0.0f, qo = 0.0f;
-    if (any) {
-        uint32_t wo = w[0];
-#pragma unroll
-        for (int i = 1; i < 4; ++i) wo = (o >> 1) == i ? w[i] : wo;
-        vo = __uint_as_float((o & 1) ? (wo & 0xFFFF0000u) : (wo << 16));
-        qo = div_fast(vo, L.so, L.ro);
-        const uint32_t ab = __float_as_uint(qo) & 0x7FFFFFFFu;
-        bad |= __builtin_amdgcn_uicmp(L.omask ? ab - kF32PowM78 : 0u, kF32Pow126 - kF32PowM78, kCmpUGE) &
-               __builtin_amdgcn_uicmp(ab, 0u, kCmpNE);
-    }
+    const uint64_t bad = __builtin_amdgcn_uicmp(__float_as_uint(a0), lim, kCmpUGE) |
+                         __builtin_amdgcn_uicmp(qb - 1u, kF32PowM74 - 1u, kCmpULT);
     if (bad) {
         aq = 0.0f;
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {             // rare: kept small
+            const uint32_t wi = i == 0 ? w[0] : i == 1 ? w[1] : i == 2 ? w[2] : w[3];
+            float lo = 0.0f, hi = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t wi = w[i >> 1];
-            const float x = (L.omask >> i) & 1u ? 0.0f : __uint_as_float((i & 1) ? (wi & 0xFFFF0000u) : (wi << 16));
-            q[i] = __fdiv_rn(x, L.s[i]);
-            aq = fmaxf(aq, __builtin_fabsf(q[i]));
+            for (int k = 0; k < 4; ++k)
+                if (k == i) {
+                    lo = keep >> (8 * k) & 1u ? __fdiv_rn(__uint_as_float(wi << 16), s[2 * k]) : 0.0f;
+                    hi = keep >> (8 * k + 4) & 1u ? __fdiv_rn(__uint_as_float(wi & 0xFFFF0000u), s[2 * k + 1]) : 0.0f;
+                }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                q[2 * k] = k == i ? lo : q[2 * k];
+                q[2 * k + 1] = k == i ? hi : q[2 * k + 1];
+            }
+            aq = fmaxf(aq, fmaxf(__builtin_fabsf(lo), __builtin_fabsf(hi)));
         }
         qb = quad_max_bits(__float_as_uint(aq));
-        if (any) qo = __fdiv_rn(vo, L.so);
-    }
-    if (any) {
-        auto column = [](int p) { return (p >> 4) * kFragBlock + ((p >> 3) & 1) * 512 + 2 * (p & 7); };
-        if (L.omask) *reinterpret_cast<uint16_t*>(xo + column(L.op)) = (uint16_t)f32_to_bf16_rne(qo);
-        for (uint32_t mm = L.omask & (L.omask - 1); mm; mm &= mm - 1) {      // further ones of the thread
-            const int i = __builtin_ctz(mm);
-            uint32_t wi = w[0];
-#pragma unroll
-            for (int c = 1; c < 4; ++c) wi = (i >> 1) == c ? w[c] : wi;
-            const float x = __uint_as_float((i & 1) ? (wi & 0xFFFF0000u) : (wi << 16));
-            *reinterpret_cast<uint16_t*>(xo + column(g.pos[j0 + i])) = (uint16_t)f32_to_bf16_rne(__fdiv_rn(x, g.s[j0 + i]));
-        }
     }
     const int32_t sb = __builtin_elementwise_max((int32_t)(qb & 0x7F800000u) - (2 << 23), 0x00200000);
     const float scale = __int_as_float(sb);
@@ -566,7 +535,7 @@ __device__ __forceinline__ uint32_t quant8(const NormQuantArgs& g, const QuantLa
     MG_CVT_FP4X2(word, q[2], q[3], scale, 1);
     MG_CVT_FP4X2(word, q[4], q[5], scale, 2);
     MG_CVT_FP4X2(word, q[6], q[7], scale, 3);
-    return word & L.nkeep;
+    return word & keep;
 }
 
 // The norm's and the modulation's arguments, read from the kernel-argument
@@ -598,6 +567,46 @@ __device__ __forceinline__ FoldArgs fold_args() {
     return f;
 }
 
+// Outlier columns are formed apart from the bulk, a lane per column of XO: its
+// channel's value is read again (the row has just been loaded), normed,
+// rounded and divided like every other's, so 64 of them cost one wave some 40
+// instructions and are stored as whole pieces.  Columns k ... 16 nso - 1 are
+// pads holding 0.
+struct OutlierLane {
+    int j, at;                      // channel (-1: a pad column), byte offset of the column in a row's part of XO (-1: none)
+    float s, a, c;
+};
+__device__ __forceinline__ OutlierLane outlier_lane(const NormQuantArgs& g, int col, int cols) {
+    OutlierLane o;
+    o.j = col < g.k ? g.O[col] : -1;
+    o.at = col < cols ? (col >> 4) * kFragBlock + ((col >> 3) & 1) * 512 + 2 * (col & 7) : -1;
+    o.s = o.j >= 0 ? g.s[o.j] : 1.0f;
+    o.a = 0.0f;
+    o.c = 0.0f;
+    return o;
+}
+// a and c of its channel, as fold8 forms them
+__device__ __forceinline__ void outlier_fold(OutlierLane& o, const FoldArgs& f, int row) {
+    const int j = o.j < 0 ? 0 : o.j;
+    float a = 1.0f, c = 0.0f;
+    if (f.mod.scale) a = 1.0f + load_elem(f.mod.scale, row * f.mod.ld + j, f.mod.dtype);
+    if (f.mod.shift) c = load_elem(f.mod.shift, row * f.mod.ld + j, f.mod.dtype);
+    if (f.norm.bias) c = __builtin_fmaf(load_elem(f.norm.bias, j, f.norm.dtype), a, c);
+    if (f.norm.weight) a *= load_elem(f.norm.weight, j, f.norm.dtype);
+    o.a = a;
+    o.c = c;
+}
+__device__ __forceinline__ void outlier_put(const OutlierLane& o, float x, float mean, float rstd, bool pad, uint8_t* xo) {
+    if (o.at < 0) return;
+    const float h = __builtin_fmaf(__builtin_fmaf(x, rstd, -mean * rstd), o.a, o.c);
+    const float q = __fdiv_rn(bf16_to_f32(pack_bf16(h, 0.0f) & 0xFFFFu), o.s);
+    *reinterpret_cast<uint16_t*>(xo + o.at) = o.j < 0 || pad ? 0 : (uint16_t)f32_to_bf16_rne(q);
+}
+template <typename XT>
+__device__ __forceinline__ float outlier_x(const XT* row, const OutlierLane& o) {
+    return o.j < 0 ? 0.0f : load_elem(row, o.j, sizeof(XT) == 4 ? MG_F32 : MG_BF16);
+}
+
 // A unit's rows r0 ... r0 + R - 1 from their staged codes (`live` of them; zeros
 // for pad rows) to Aq and As, and the pad rows of XO, by T threads: 16-byte
 // pieces, rows fastest, R of them contiguous in memory.
@@ -605,26 +614,29 @@ template <int FIXED>
 __device__ __forceinline__ void flush_unit(const NormQuantArgs& g, int64_t r0, int live, int64_t M32, int64_t ns4, int64_t nso,
                                            int nwin, const uint8_t* stA, int rowA, const uint8_t* stS, int rowS, int T,
                                            int R_ = FIXED) {
-    const int R = FIXED ? FIXED : R_, tid = threadIdx.x;
+    const int R = FIXED ? FIXED : R_, sh = FIXED ? 3 : 31 - __builtin_clz(R), tid = threadIdx.x;
     const int rows = M32 - r0 < R ? (M32 > r0 ? (int)(M32 - r0) : 0) : R;
     const u32x4 zero = {0, 0, 0, 0};
     uint8_t* const aq = g.Aq + (r0 >> 5) * ns4 * kFragBlock + ((r0 & 31) << 4);
+#pragma unroll 2
     for (int i = tid; i < (int)ns4 * 2 * R; i += T) {
-        const int rr = i & (R - 1), line = i / R;
+        const int rr = i & (R - 1), line = i >> sh;
         if (rr < rows)
             *reinterpret_cast<u32x4*>(aq + (line >> 1) * kFragBlock + (line & 1) * 512 + rr * 16) =
                 rr < live ? *reinterpret_cast<const u32x4*>(stA + rr * rowA + line * 16) : zero;
     }
     uint8_t* const as = g.As + (r0 / kScRows) * nwin * kScWinBytes + (r0 % kScRows) * kScBlocks;
+#pragma unroll 1
     for (int i = tid; i < nwin * R; i += T) {
-        const int rr = i & (R - 1), win = i / R;
+        const int rr = i & (R - 1), win = i >> sh;
         *reinterpret_cast<u32x4*>(as + (int64_t)win * kScWinBytes + rr * kScBlocks) =
             rr < live ? *reinterpret_cast<const u32x4*>(stS + rr * rowS + win * 16) : zero;
     }
     if (live < rows) {
         uint8_t* const xo = g.XO + (r0 >> 5) * nso * kFragBlock + ((r0 & 31) << 4);
+#pragma unroll 1
         for (int i = tid; i < (int)nso * 2 * R; i += T) {
-            const int rr = i & (R - 1), line = i / R;
+            const int rr = i & (R - 1), line = i >> sh;
             if (rr >= live && rr < rows)
                 *reinterpret_cast<u32x4*>(xo + (line >> 1) * kFragBlock + (line & 1) * 512 + rr * 16) = zero;
         }
@@ -644,20 +656,16 @@ norm_quant_kernel(NormQuantArgs g, int R) {
     extern __shared__ __attribute__((aligned(16))) uint8_t stage[];   // R rows: codes (256 bytes a window, 16 pad), scales (16)
     int turn = 0;
     const RowArgs& a = g.r;
-    const int K = a.K, nwin = (int)sc_nwin(K), tid = threadIdx.x;
+    const int K = a.K, nwin = (int)sc_nwin(K), lane = (int)threadIdx.x & 63;
     const RowThread<V, false> t(K);
     const XT* X = static_cast<const XT*>(a.X);
     const int64_t ns4 = frag_slices(K / 2), nso = frag_slices(2 * (int64_t)g.k);
     const int64_t M = a.M, M32 = (M + 31) / 32 * 32, Mp = (M + kScRows - 1) / kScRows * kScRows;
-    const int rowA = nwin * 256 + 16, rowS = nwin * 16;
+    const int rowA = nwin * 256 + 16, rowS = nwin * 16, cols = 16 * (int)nso;
     uint8_t* const stS = stage + (size_t)R * rowA;
     float na[KEEP ? V : 1][8], nc[KEEP ? V : 1][8];
     QuantLane ql[KEEP ? V : 1];
     int mi_of = -1, mrow = -1;
-    if constexpr (KEEP) {
-#pragma unroll
-        for (int v = 0; v < V; ++v) ql[v] = quant_lane(g, t.col[v], t.col[v] < K);
-    }
     Raw8<XT> rx[V];
     auto load_row = [&](int64_t r) {
         r = r < M ? r : M - 1;
@@ -667,26 +675,44 @@ norm_quant_kernel(NormQuantArgs g, int R) {
     };
     const int64_t step = (int64_t)gridDim.x * R;
     int64_t r0 = (int64_t)blockIdx.x * R;
-    if (KEEP) load_row(r0);
+    if (r0 < M) {
+        if (KEEP) load_row(r0);
+        if constexpr (KEEP) {
+#pragma unroll
+            for (int v = 0; v < V; ++v) quant_lane(g, t.col[v], t.col[v] < K, ql[v]);
+        }
+    }
+    OutlierLane ol = outlier_lane(g, 64 * t.wave + lane, cols);       // this wave's first 64 columns
     for (; r0 < Mp; r0 += step) {
         const int live = r0 >= M ? 0 : M - r0 < R ? (int)(M - r0) : R;
         for (int rr = 0; rr < live; ++rr) {
             const int64_t r = r0 + rr;
             if constexpr (!KEEP) load_row(r);
             const int mi = __builtin_amdgcn_readfirstlane(mrow);
-            if (KEEP && mi >= 0 && mi != mi_of) {
+            if (mi >= 0 && mi != mi_of) {
                 const FoldArgs f = fold_args();
+                if constexpr (KEEP) {
 #pragma unroll
-                for (int v = 0; v < V; ++v) fold8(t, f.norm, f.mod, mi, v, na[v], nc[v]);
+                    for (int v = 0; v < V; ++v) fold8(t, f.norm, f.mod, mi, v, na[v], nc[v]);
+                }
+                outlier_fold(ol, f, mi);
                 mi_of = mi;
             }
             float x[V][8];
 #pragma unroll
             for (int v = 0; v < V; ++v) unpack(rx[v], x[v]);
+            const float xo0 = outlier_x(X + r * a.ldx, ol);
             if constexpr (KEEP) load_row(rr + 1 < live ? r + 1 : r0 + step);
             float mean, rstd;
             row_stats(x, t, a.norm.kind, a.norm.eps, pairs, turn, mean, rstd);
             uint8_t* const xo = g.XO + (r >> 5) * nso * kFragBlock + ((r & 31) << 4);
+            outlier_put(ol, xo0, mean, rstd, mi < 0, xo);
+#pragma unroll 1
+            for (int c = 64 * (t.wave + t.W); c < cols; c += 64 * t.W) {
+                OutlierLane o = outlier_lane(g, c + lane, cols);
+                if (mi >= 0) outlier_fold(o, fold_args(), mi);
+                outlier_put(o, outlier_x(X + r * a.ldx, o), mean, rstd, mi < 0, xo);
+            }
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 const int win = v * t.W + t.wave;
@@ -694,23 +720,20 @@ norm_quant_kernel(NormQuantArgs g, int R) {
                 if constexpr (!KEEP) {
                     const FoldArgs f = fold_args();
                     fold8(t, f.norm, f.mod, mi < 0 ? 0 : mi, v, na[0], nc[0]);
-                    ql[0] = quant_lane(g, t.col[v], t.col[v] < K);
+                    quant_lane(g, t.col[v], t.col[v] < K, ql[0]);
                 }
                 apply8(x[v], mean, rstd, na[KEEP ? v : 0], nc[KEEP ? v : 0]);
                 u32x4 w = pack8_bf16(x[v]);
-                const bool on = mi >= 0 && t.col[v] < K;              // K % 32 == 0: whole blocks
+                if (mi < 0 || !(t.full >> v & 1u)) {                  // K % 32 == 0: whole blocks
+                    const bool on = mi >= 0 && t.col[v] < K;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) w[i] = on ? w[i] : 0u;
+                    for (int i = 0; i < 4; ++i) w[i] = on ? w[i] : 0u;
+                }
                 uint32_t code;
                 const QuantLane& L = ql[KEEP ? v : 0];
-                const uint32_t word = quant8(g, L, w, t.col[v], xo, code, __builtin_amdgcn_ballot_w64(L.omask != 0) != 0);
-                const int l = tid & 63;
-                *reinterpret_cast<uint32_t*>(stage + rr * rowA + win * 256 + 4 * l) = word;
-                if ((l & 3) == 0) stS[rr * rowS + win * 16 + sc_pos(l >> 2)] = (uint8_t)code;
-            }
-            if (tid < 16 * (int)nso - g.k) {                          // pad columns of XO
-                const int p = g.k + tid;
-                *reinterpret_cast<uint16_t*>(xo + (p >> 4) * kFragBlock + ((p >> 3) & 1) * 512 + 2 * (p & 7)) = 0;
+                const uint32_t word = quant8(L.s, L.rz, L.keep, L.lim, w, code);
+                *reinterpret_cast<uint32_t*>(stage + rr * rowA + win * 256 + 4 * lane) = word;
+                if ((lane & 3) == 0) stS[rr * rowS + win * 16 + sc_pos(lane >> 2)] = (uint8_t)code;
             }
         }
         if (live) __syncthreads();                                    // the unit's codes are staged
@@ -718,33 +741,35 @@ norm_quant_kernel(NormQuantArgs g, int R) {
     }
 }
 
-
 // The same with a row per wave, for up to 5120 channels and many rows: the
-// per-channel constants (a, c, s, 1 / s: 16 bytes a channel, and the outlier
-// routing) lie in LDS, once for the 8 waves of the workgroup, a row needs no
-// barrier and one wave's bookkeeping instead of W waves', and its registers
-// are refilled window by window with the next row.  V: windows of 512 channels.
-// The sums are row_kernel's (those of its W waves, one after the other), so
+// per-channel constants (a, c, s, 1 / s: 16 bytes a channel) lie in LDS, once
+// for the 8 waves of the workgroup, a row needs no barrier and one wave's
+// bookkeeping instead of W waves', and its registers are refilled window by
+// window with the next row.  V: windows of 512 channels, of which only the
+// last can be partial.  The sums are row_kernel's (those of its W waves), so
 // the bits are.
 template <int V>
 struct WaveShape {
     static constexpr int W = V <= 8 ? V : (V + 1) / 2;             // row_kernel's waves (and one or two vectors) for V windows
     static constexpr int rowA = V * 256 + 16, rowS = V * 16;       // staged bytes of a row: codes, scales
-    static constexpr int lds = V * 64 * 144 + 2 * 8 * (rowA + rowS);
+    static constexpr int consts = V * 64 * 136;                    // a, c, s, rz, and keep and lim
+    static constexpr int lds = consts + 2 * 8 * (rowA + rowS);
 };
 template <int V, typename XT>
 __global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) norm_quant_wave_kernel(NormQuantArgs g) {
     using S = WaveShape<V>;
     extern __shared__ __attribute__((aligned(16))) uint8_t stage[];
-    float4* const ka = reinterpret_cast<float4*>(stage);            // a, c, s, rz: [array][window][half][lane]
-    uint4* const ko = reinterpret_cast<uint4*>(stage + V * 64 * 128);  // nkeep, XO column, s and 1 / s of the first outlier
-    uint8_t* const st = stage + V * 64 * 144;
+    float4* const ka = reinterpret_cast<float4*>(stage);              // [array a, c, s, rz][window][half][lane]
+    uint2* const kk = reinterpret_cast<uint2*>(stage + V * 64 * 128);  // [window][lane] keep, lim
+    uint8_t* const st = stage + S::consts;
     const RowArgs& a = g.r;
-    const int K = a.K, nwin = (int)sc_nwin(K), tid = threadIdx.x, lane = tid & 63;
+    const int K = a.K, tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const XT* X = static_cast<const XT*>(a.X);
     const int64_t ns4 = frag_slices(K / 2), nso = frag_slices(2 * (int64_t)g.k);
     const int64_t M = a.M, M32 = (M + 31) / 32 * 32, Mp = (M + kScRows - 1) / kScRows * kScRows;
+    const int cols = 16 * (int)nso;
+    const bool last_in = 512 * (V - 1) + 8 * lane < K;               // the lane's channels of the last window exist
     auto slot = [&](int arr, int win, int half, int l) -> float4& { return ka[((arr * V + win) * 2 + half) * 64 + l]; };
     auto put8 = [&](int arr, int win, int l, const float (&v)[8]) {
         slot(arr, win, 0, l) = make_float4(v[0], v[1], v[2], v[3]);
@@ -761,47 +786,42 @@ __global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) n
         t.at[0] = t.col[0] < K - 8 ? t.col[0] : K - 8;
     };
     for (int i = tid; i < V * 64; i += 512) {
-        const int win = i >> 6, l = i & 63, j0 = i * 8;
-        const QuantLane q = quant_lane(g, j0, j0 < K);
-        put8(2, win, l, q.s);
-        put8(3, win, l, q.rz);
-        ko[i] = make_uint4(q.nkeep, (uint32_t)q.op, __float_as_uint(q.so), __float_as_uint(q.ro));
+        QuantLane q;
+        quant_lane(g, i * 8, i * 8 < K, q);
+        put8(2, i >> 6, i & 63, q.s);
+        put8(3, i >> 6, i & 63, q.rz);
+        kk[i] = make_uint2(q.keep, q.lim);
     }
-    __syncthreads();
-    uint32_t outl = 0, slow = 0;        // windows with an outlier channel; whose s is out of the fast division's range
-    for (int win = 0; win < V; ++win) {
-        float s[8];
-        get8(2, win, s);
-        bool ok = true;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ok &= div_fast_ok_s(s[i]);
-        outl |= (__builtin_amdgcn_ballot_w64(ko[win * 64 + lane].x != 0xFFFFFFFFu) ? 1u : 0u) << win;
-        slow |= (__builtin_amdgcn_ballot_w64(!ok) ? 1u : 0u) << win;
-    }
-    // channels of row_kernel's waves: the lane's (lane % 16), and its own share of each
-    float nl, rnl;
-    {
+    OutlierLane ol = outlier_lane(g, lane, cols);
+    // channels of row_kernel's wave w: windows w, w + W, ...
+    auto count = [&](int w) {
         int c = 0;
+#pragma unroll
         for (int v = 0; v * S::W < V; ++v) {
-            const int l = K - 512 * (v * S::W + (lane & 15));
-            c += (lane & 15) >= S::W || l < 0 ? 0 : l < 512 ? l : 512;
+            const int l = K - 512 * (v * S::W + w);
+            c += l < 0 ? 0 : l < 512 ? l : 512;
         }
-        nl = (float)c;
-        rnl = c ? 1.0f / (float)c : 0.0f;
-    }
-    const float rK = 1.0f / (float)K;
+        return c;
+    };
+    const int cl = (lane & 15) < S::W ? count(lane & 15) : 0;
+    const float nl = (float)cl, rnl = cl ? 1.0f / (float)cl : 0.0f, rK = 1.0f / (float)K;
     const bool layer = a.norm.kind == MG_NORM_LAYER;
     const float eps = a.norm.eps;
     int loaded = -1, turn = 0;
     Raw8<XT> rx[V];
-    auto load_win = [&](int64_t r, int v) {
+    auto load_win = [&](const XT* row, int v) {
         const int col = 512 * v + 8 * lane;
-        load_raw(X + (r < M ? r : M - 1) * a.ldx + (col < K - 8 ? col : K - 8), rx[v]);
+        load_raw(row + (v < V - 1 || col < K - 8 ? col : K - 8), rx[v]);
     };
+    auto row_at = [&](int64_t r) { return X + (r < M ? r : M - 1) * a.ldx; };
     const int64_t step = (int64_t)gridDim.x * 8;
     int64_t r0 = (int64_t)blockIdx.x * 8;
+    {
+        const XT* row = row_at(r0 + wave);
 #pragma unroll
-    for (int v = 0; v < V; ++v) load_win(r0 + wave, v);
+        for (int v = 0; v < V; ++v) load_win(row, v);
+    }
+    float xo0 = outlier_x(row_at(r0 + wave), ol);
     auto mod_rows = [&](int64_t r) { return lane < 8 && r + lane < M ? mod_row(a.mod, r + lane) : -1; };
     int mis = mod_rows(r0);
     for (; r0 < Mp; r0 += step) {
@@ -814,6 +834,7 @@ __global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) n
         if (want != loaded) {           // the same in every wave
             __syncthreads();
             const FoldArgs f = fold_args();
+#pragma unroll 1
             for (int i = tid; i < V * 64; i += 512) {
                 float na[8], nc[8];
                 at_window(i >> 6, i & 63);
@@ -821,99 +842,124 @@ __global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) n
                 put8(0, i >> 6, i & 63, na);
                 put8(1, i >> 6, i & 63, nc);
             }
+            outlier_fold(ol, f, want);
             __syncthreads();
             loaded = want;
         }
         uint8_t* const stA = st + turn * 8 * (S::rowA + S::rowS), * const stS = stA + 8 * S::rowA;
         if (wave < live) {
-            // the sums of row_kernel's wave w: windows w, w + W
-            float s = 0.0f, q = 0.0f;   // of wave (lane % 16)
             float x[V][8];
 #pragma unroll
             for (int v = 0; v < V; ++v) unpack(rx[v], x[v]);
-            auto count = [&](int w) {   // channels of wave w
-                int c = 0;
+            // sums of row_kernel's waves, step by step side by side
+            float sw[S::W], qw[S::W], m[S::W];
+            auto sums = [&](float (&u)[S::W]) {
 #pragma unroll
-                for (int v = 0; v * S::W < V; ++v) {
-                    const int l = K - 512 * (v * S::W + w);
-                    c += l < 0 ? 0 : l < 512 ? l : 512;
-                }
-                return c;
+                for (int w = 0; w < S::W; ++w) u[w] = dpp_add<0xB1, 0xF>(u[w]);
+#pragma unroll
+                for (int w = 0; w < S::W; ++w) u[w] = dpp_add<0x4E, 0xF>(u[w]);
+#pragma unroll
+                for (int w = 0; w < S::W; ++w) u[w] = dpp_add<0x141, 0xF>(u[w]);
+#pragma unroll
+                for (int w = 0; w < S::W; ++w) u[w] = dpp_add<0x140, 0xF>(u[w]);
+#pragma unroll
+                for (int w = 0; w < S::W; ++w) u[w] = dpp_add<0x142, 0xA>(u[w]);
+#pragma unroll
+                for (int w = 0; w < S::W; ++w) u[w] = dpp_add<0x143, 0xC>(u[w]);
+#pragma unroll
+                for (int w = 0; w < S::W; ++w) u[w] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(u[w]), 63));
             };
 #pragma unroll
             for (int w = 0; w < S::W; ++w) {
-                float sw = 0.0f, qw = 0.0f, m = 0.0f;
+                sw[w] = 0.0f;
+                m[w] = 0.0f;
                 if (layer) {
 #pragma unroll
                     for (int v = w; v < V; v += S::W)
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) sw += 512 * v + 8 * lane < K ? x[v][i] : 0.0f;
-                    sw = wave_sum(sw);
-                    const int c = count(w);
-                    m = sw * (c ? 1.0f / (float)c : 0.0f);
+                        for (int i = 0; i < 8; ++i) sw[w] += v < V - 1 || last_in ? x[v][i] : 0.0f;
                 }
+            }
+            if (layer) {
+                sums(sw);
+#pragma unroll
+                for (int w = 0; w < S::W; ++w) {
+                    const int c = count(w);
+                    m[w] = sw[w] * (c ? 1.0f / (float)c : 0.0f);
+                }
+            }
+#pragma unroll
+            for (int w = 0; w < S::W; ++w) {
+                qw[w] = 0.0f;
 #pragma unroll
                 for (int v = w; v < V; v += S::W)
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
-                        const float d = 512 * v + 8 * lane < K ? x[v][i] - m : 0.0f;
-                        qw = __builtin_fmaf(d, d, qw);
+                        const float d = v < V - 1 || last_in ? x[v][i] - m[w] : 0.0f;
+                        qw[w] = __builtin_fmaf(d, d, qw[w]);
                     }
-                qw = wave_sum(qw);
-                s = (lane & 15) == w ? sw : s;
-                q = (lane & 15) == w ? qw : q;
+            }
+            sums(qw);
+            float s = 0.0f, q = 0.0f;   // of wave (lane % 16)
+#pragma unroll
+            for (int w = 0; w < S::W; ++w) {
+                s = (lane & 15) == w ? sw[w] : s;
+                q = (lane & 15) == w ? qw[w] : q;
             }
             const float mean = layer ? row16_sum(s) * rK : 0.0f;
             const float d = s * rnl - mean;
             const float rstd = rsqrt_f32(__builtin_fmaf(row16_sum(__builtin_fmaf(nl * d, d, q)), rK, eps));
             uint8_t* const xo = g.XO + (r >> 5) * nso * kFragBlock + ((r & 31) << 4);
+            const bool own = mi != loaded && mi >= 0;                 // another modulation row than the unit's
+            {
+                OutlierLane o = ol;
+                if (own) outlier_fold(o, fold_args(), mi);
+                outlier_put(o, xo0, mean, rstd, mi < 0, xo);
+#pragma unroll 1
+                for (int c = 64; c < cols; c += 64) {
+                    o = outlier_lane(g, c + lane, cols);
+                    if (mi >= 0) outlier_fold(o, fold_args(), mi);
+                    outlier_put(o, outlier_x(row_at(r), o), mean, rstd, mi < 0, xo);
+                }
+                xo0 = outlier_x(row_at(r + step), ol);
+            }
+            const XT* next = row_at(r + step);
+            uint8_t* const stw = stA + wave * S::rowA + 4 * lane;
+            uint8_t* const sts = stS + wave * S::rowS + sc_pos(lane >> 2);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
-                const int j0 = 512 * v + 8 * lane;
                 float na[8], nc[8];
-                if (mi == loaded || mi < 0) {
-                    get8(0, v, na);
-                    get8(1, v, nc);
-                } else {
+                if (own) {
                     const FoldArgs f = fold_args();
                     at_window(v, lane);
                     fold8(t, f.norm, f.mod, mi, 0, na, nc);
+                } else {
+                    get8(0, v, na);
+                    get8(1, v, nc);
                 }
                 apply8(x[v], mean, rstd, na, nc);
                 u32x4 w = pack8_bf16(x[v]);
-                const bool on = mi >= 0 && j0 < K;
+                load_win(next, v);
+                if (v == V - 1 || mi < 0) {
+                    const bool on = mi >= 0 && (v < V - 1 || last_in);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) w[i] = on ? w[i] : 0u;
-                load_win(r + step, v);
-                QuantLane L;
-                get8(2, v, L.s);
-                get8(3, v, L.rz);
-                const uint4 o = ko[v * 64 + lane];
-                L.nkeep = o.x;
-                L.op = (int)o.y;
-                L.so = __uint_as_float(o.z);
-                L.ro = __uint_as_float(o.w);
-                L.omask = 0;
-                if (outl >> v & 1u) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) L.omask |= ((o.x >> (4 * i) & 1u) ^ 1u) << i;
+                    for (int i = 0; i < 4; ++i) w[i] = on ? w[i] : 0u;
                 }
-                L.lim = __uint_as_float(slow >> v & 1u ? 0u : kF32Pow126);
+                float s8[8], rz[8];
+                get8(2, v, s8);
+                get8(3, v, rz);
+                const uint2 kl = kk[v * 64 + lane];
                 uint32_t code;
-                const uint32_t word = quant8(g, L, w, j0, xo, code, outl >> v & 1u);
-                *reinterpret_cast<uint32_t*>(stA + wave * S::rowA + v * 256 + 4 * lane) = word;
-                if ((lane & 3) == 0) stS[wave * S::rowS + v * 16 + sc_pos(lane >> 2)] = (uint8_t)code;
-            }
-            if (lane < 16 * (int)nso - g.k) {                       // pad columns of XO
-                const int p = g.k + lane;
-                *reinterpret_cast<uint16_t*>(xo + (p >> 4) * kFragBlock + ((p >> 3) & 1) * 512 + 2 * (p & 7)) = 0;
+                const uint32_t word = quant8(s8, rz, kl.x, kl.y, w, code);
+                *reinterpret_cast<uint32_t*>(stw + v * 256) = word;
+                if ((lane & 3) == 0) sts[v * 16] = (uint8_t)code;
             }
         }
         // one barrier a unit: the next unit stages into the other half, and is
         // past its barrier only when every wave has left this one's
         if (live) __syncthreads();
         turn ^= 1;
-        flush_unit<8>(g, r0, live, M32, ns4, nso, nwin, stA, S::rowA, stS, S::rowS, 512);
+        flush_unit<8>(g, r0, live, M32, ns4, nso, V, stA, S::rowA, stS, S::rowS, 512);
     }
 }
 

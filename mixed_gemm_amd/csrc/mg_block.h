@@ -52,6 +52,7 @@ struct NormQuantArgs {
     const float* s;
     const float* rcp;
     const int32_t* pos;
+    const int32_t* O;
     uint8_t* Aq;
     uint8_t* As;
     uint8_t* XO;

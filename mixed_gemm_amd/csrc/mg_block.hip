@@ -223,7 +223,7 @@ int mg_norm_quantize_act(const mg_plan* p, const mg_norm* norm, const mg_mod* mo
     if (int e = check_act(p, a)) return e;
     q.r.X = X; q.r.ldx = ldx; q.r.M = M; q.r.K = K; q.r.x_dtype = dtype; q.r.has_norm = 1;
     q.r.gate.group = 0x7FFFFFFFu;
-    q.s = p->s; q.rcp = p->rcp; q.pos = p->pos; q.k = p->d.k;
+    q.s = p->s; q.rcp = p->rcp; q.pos = p->pos; q.O = p->O; q.k = p->d.k;
     q.Aq = a->Aq; q.As = a->As; q.XO = reinterpret_cast<uint8_t*>(a->XO);
     return hip_status(launch_norm_quant(q, stream), "mg_norm_quantize_act");
 }
