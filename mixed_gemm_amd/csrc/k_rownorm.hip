@@ -68,6 +68,28 @@ __device__ __forceinline__ void unpack(const Raw8<T>& r, float (&v)[8]) {
     }
 }
 
+// The same of a type known at run time (null pointer: nothing).  Loading and
+// using are apart, so that the loads of several arrays are in flight together.
+struct RawAny {
+    u32x4 d[2];
+};
+__device__ __forceinline__ void load_any(const void* p, int64_t at, int32_t dtype, RawAny& r) {
+    if (p == nullptr) return;
+    if (dtype == MG_F32) {
+        const Piece16* q = reinterpret_cast<const Piece16*>(static_cast<const float*>(p) + at);
+        r.d[0] = q[0].v;
+        r.d[1] = q[1].v;
+    } else {
+        r.d[0] = reinterpret_cast<const Piece16*>(static_cast<const uint16_t*>(p) + at)->v;
+    }
+}
+__device__ __forceinline__ void unpack(const RawAny& r, int32_t dtype, float (&v)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        v[i] = __uint_as_float(dtype == MG_F32 ? r.d[i >> 2][i & 3]
+                                               : i & 1 ? r.d[0][i >> 1] & 0xFFFF0000u : r.d[0][i >> 1] << 16);
+}
+
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 // two floats rounded to bf16 (nearest even, NaN kept), the first in the low half
@@ -134,15 +156,9 @@ struct RowThread {
     }
     // 8 values of a [K] array of either type
     __device__ __forceinline__ void load8(const void* p, int64_t row, int32_t dtype, int v, float (&x)[8]) const {
-        if (dtype == MG_F32) {
-            Raw8<float> r;
-            load_raw(static_cast<const float*>(p) + row + at[v], r);
-            unpack(r, x);
-        } else {
-            Raw8<uint16_t> r;
-            load_raw(static_cast<const uint16_t*>(p) + row + at[v], r);
-            unpack(r, x);
-        }
+        RawAny r;
+        load_any(p, row + at[v], dtype, r);
+        unpack(r, dtype, x);
         place(v, x);
     }
     __device__ __forceinline__ void store8(void* p, int64_t row, int32_t dtype, int v, const float (&x)[8]) const {
@@ -245,27 +261,60 @@ __device__ __forceinline__ void row_stats(const float (&x)[V][8], const RowThrea
 
 // A norm with its modulation folded to n a + c, n = (x - mean) rstd: a = w (1 +
 // scale_i), c = b (1 + scale_i) + shift_i of 8 channels.
+struct FoldRaw {
+    RawAny scale, shift, weight, bias;
+};
 template <int V, bool ODD>
-__device__ __forceinline__ void fold8(const RowThread<V, ODD>& t, const NormArgs& n, const ModArgs& m, int row, int v,
-                                      float (&a)[8], float (&c)[8]) {
+__device__ __forceinline__ void fold_load(const RowThread<V, ODD>& t, const NormArgs& n, const ModArgs& m, int row, int v, FoldRaw& f) {
+    load_any(m.scale, row * m.ld + t.at[v], m.dtype, f.scale);
+    load_any(m.shift, row * m.ld + t.at[v], m.dtype, f.shift);
+    load_any(n.bias, t.at[v], n.dtype, f.bias);
+    load_any(n.weight, t.at[v], n.dtype, f.weight);
+}
+template <int V, bool ODD>
+__device__ __forceinline__ void fold_make(const RowThread<V, ODD>& t, const NormArgs& n, const ModArgs& m, const FoldRaw& f, int v,
+                                          float (&a)[8], float (&c)[8]) {
     float w[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) { a[i] = 1.0f; c[i] = 0.0f; }
     if (m.scale) {
-        t.load8(m.scale, row * m.ld, m.dtype, v, w);
+        unpack(f.scale, m.dtype, w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) a[i] = 1.0f + w[i];
     }
-    if (m.shift) t.load8(m.shift, row * m.ld, m.dtype, v, c);
+    if (m.shift) unpack(f.shift, m.dtype, c);
     if (n.bias) {
-        t.load8(n.bias, 0, n.dtype, v, w);
+        unpack(f.bias, n.dtype, w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) c[i] = __builtin_fmaf(w[i], a[i], c[i]);
     }
     if (n.weight) {
-        t.load8(n.weight, 0, n.dtype, v, w);
+        unpack(f.weight, n.dtype, w);
 #pragma unroll
         for (int i = 0; i < 8; ++i) a[i] *= w[i];
+    }
+    t.place(v, a);
+    t.place(v, c);
+}
+template <int V, bool ODD>
+__device__ __forceinline__ void fold8(const RowThread<V, ODD>& t, const NormArgs& n, const ModArgs& m, int row, int v,
+                                      float (&a)[8], float (&c)[8]) {
+    FoldRaw f;
+    fold_load(t, n, m, row, v, f);
+    fold_make(t, n, m, f, v, a, c);
+}
+// of all vectors, two at a time
+template <int V, bool ODD>
+__device__ __forceinline__ void fold_all(const RowThread<V, ODD>& t, const NormArgs& n, const ModArgs& m, int row,
+                                         float (&a)[V][8], float (&c)[V][8]) {
+    constexpr int G = V < 2 ? 1 : 2;
+#pragma unroll
+    for (int v = 0; v < V; v += G) {
+        FoldRaw f[G];
+#pragma unroll
+        for (int k = 0; k < G; ++k) fold_load(t, n, m, row, v + k, f[k]);
+#pragma unroll
+        for (int k = 0; k < G; ++k) fold_make(t, n, m, f[k], v + k, a[v + k], c[v + k]);
     }
 }
 // n a + c; the rounding of -mean rstd is as small as the mean's own
@@ -351,15 +400,27 @@ row_kernel(RowArgs a, RowSpan span) {
     while (true) {
         const int mi = __builtin_amdgcn_readfirstlane(mrow), gi = __builtin_amdgcn_readfirstlane(grow);
         if constexpr (KEEP) {
-            if (RES && gi >= 0 && gi != gi_of) {
+            const bool ng = RES && gi >= 0 && gi != gi_of;
+            RawAny rg[V];
+            if (ng) {
 #pragma unroll
-                for (int v = 0; v < V; ++v) load_or_1(t, a.gate.gate, gi * a.gate.ld, a.gate.dtype, v, ga[RES ? v : 0]);
+                for (int v = 0; v < V; ++v) load_any(a.gate.gate, gi * a.gate.ld + t.at[v], a.gate.dtype, rg[v]);
                 gi_of = gi;
             }
             if (mi >= 0 && mi != mi_of) {
-#pragma unroll
-                for (int v = 0; v < V; ++v) fold8(t, a.norm, a.mod, mi, v, na[v], nc[v]);
+                fold_all(t, a.norm, a.mod, mi, na, nc);
                 mi_of = mi;
+            }
+            if (ng) {
+#pragma unroll
+                for (int v = 0; v < V; ++v) {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) ga[RES ? v : 0][i] = 1.0f;
+                    if (a.gate.gate) {
+                        unpack(rg[v], a.gate.dtype, ga[RES ? v : 0]);
+                        t.place(v, ga[RES ? v : 0]);
+                    }
+                }
             }
         }
         float x[V][8], y[RES ? V : 1][8];
@@ -475,11 +536,19 @@ struct QuantLane {
 __device__ __forceinline__ void quant_lane(const NormQuantArgs& g, int j0, bool in, QuantLane& q) {
     bool ok = true;
     q.keep = 0xFFFFFFFFu;
+    const int j = in ? j0 : 0;         // 32-byte pieces of the plan's vectors
+    const float4* ps = reinterpret_cast<const float4*>(g.s + j);
+    const float4* pr = reinterpret_cast<const float4*>(g.rcp + j);
+    const int4* pp = reinterpret_cast<const int4*>(g.pos + j);
+    const float4 s0 = ps[0], s1 = ps[1], r0 = pr[0], r1 = pr[1];
+    const int4 p0 = pp[0], p1 = pp[1];
+    const float s[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w}, r[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
+    const int p[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        q.s[i] = in ? g.s[j0 + i] : 1.0f;
-        const bool out = in && g.pos[j0 + i] >= 0;
-        q.rz[i] = in && !out ? g.rcp[j0 + i] : 0.0f;
+        q.s[i] = in ? s[i] : 1.0f;
+        const bool out = in && p[i] >= 0;
+        q.rz[i] = in && !out ? r[i] : 0.0f;
         q.keep &= out ? ~(0xFu << (4 * i)) : 0xFFFFFFFFu;
         ok &= div_fast_ok_s(q.s[i]);
     }
@@ -675,12 +744,10 @@ norm_quant_kernel(NormQuantArgs g, int R) {
     };
     const int64_t step = (int64_t)gridDim.x * R;
     int64_t r0 = (int64_t)blockIdx.x * R;
-    if (r0 < M) {
-        if (KEEP) load_row(r0);
-        if constexpr (KEEP) {
+    if constexpr (KEEP) {
+        load_row(r0);
 #pragma unroll
-            for (int v = 0; v < V; ++v) quant_lane(g, t.col[v], t.col[v] < K, ql[v]);
-        }
+        for (int v = 0; v < V; ++v) quant_lane(g, t.col[v], t.col[v] < K, ql[v]);
     }
     OutlierLane ol = outlier_lane(g, 64 * t.wave + lane, cols);       // this wave's first 64 columns
     for (; r0 < Mp; r0 += step) {
@@ -691,10 +758,7 @@ norm_quant_kernel(NormQuantArgs g, int R) {
             const int mi = __builtin_amdgcn_readfirstlane(mrow);
             if (mi >= 0 && mi != mi_of) {
                 const FoldArgs f = fold_args();
-                if constexpr (KEEP) {
-#pragma unroll
-                    for (int v = 0; v < V; ++v) fold8(t, f.norm, f.mod, mi, v, na[v], nc[v]);
-                }
+                if constexpr (KEEP) fold_all(t, f.norm, f.mod, mi, na, nc);
                 outlier_fold(ol, f, mi);
                 mi_of = mi;
             }
