@@ -13,10 +13,13 @@
 // ranges and read 0.  The waves' partial sums meet in LDS and are added in the
 // order of the waves, so a call's bits do not vary.
 //
-// Bound: one token, K = 5120 -> N = 13824 (35.4 MB of codes, 2.2 MB of scales)
-// takes 9.6 us, 13824 -> 5120 8.9 us, of which a launch and its host call are
-// about 7 (a 1024 x 1024 layer takes 7.9); the 256x256 tiles take 34 and 72.
-// With more tokens the operands' way into a CU bounds it (few_tile).
+// Bound: one token, K = 5120 -> N = 13824 (37.6 MB of codes and scales) takes
+// 8.3 us and 13824 -> 5120 8.4 us inside a graph, 4.5 TB/s, against 3.2 us for
+// a 1568 x 1056 layer: the weights' way from memory.  With more tokens the
+// operands' way into a CU (few_tile).  Fewer registers pay more than more
+// loads in flight: 4 waves with one or two half-windows leave room for two to
+// three workgroups on a CU, whose starts and joins overlap the others' K loops
+// (8 waves with three half-windows: 1.2 to 1.6 times as long from 32 tokens on).
 #include "gemm_epilogue.h"
 #include "mg_block.h"
 #include "mg_device.h"
@@ -75,10 +78,11 @@ __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW
     const int K = g.K, N = g.N;
     const int64_t M = g.M;
     const EpArgs& e = g.ep;
-    // workgroups go round-robin to the 8 XCDs: XCD x takes column blocks x,
-    // x + 8, ..., each with all its token blocks in a row (they share weights)
-    const int gy = (int)((M + 32 * TG - 1) / (32 * TG)), j = (int)blockIdx.x >> 3;
-    const int bx = ((int)blockIdx.x & 7) + 8 * (j / gy), by = j % gy;
+    // workgroups go round-robin to the 8 XCDs: each takes an equal run of the
+    // tiles, token blocks fastest (those of a column block share its weights)
+    const int gy = (int)((M + 32 * TG - 1) / (32 * TG));
+    const int tile = ((int)blockIdx.x & 7) * ((int)gridDim.x >> 3) + ((int)blockIdx.x >> 3);
+    const int bx = tile / gy, by = tile - bx * gy;
     const int n0 = bx * 32 * NG;
     if (n0 >= N) return;
     const int64_t t0 = (int64_t)by * 32 * TG;
@@ -271,38 +275,45 @@ hipError_t launch_few(const FewArgs& a, hipStream_t st) {
         configured_dev = dev;
     }
     const int64_t gx = (a.N + 32 * NG - 1) / (32 * NG), gy = (a.M + 32 * TG - 1) / (32 * TG);
-    hipLaunchKernelGGL((gemm_few<YT, TG, NG, NW, D>), dim3((unsigned)((gx + 7) / 8 * 8 * gy)), dim3(64 * NW), lds, st, a);
+    hipLaunchKernelGGL((gemm_few<YT, TG, NG, NW, D>), dim3((unsigned)((gx * gy + 7) / 8 * 8)), dim3(64 * NW), lds, st, a);
     return hipGetLastError();
 }
 
 template <typename YT>
 hipError_t run_few(int tile, const FewArgs& a, hipStream_t st) {
     switch (tile) {
-        case 0: return launch_few<YT, 1, 1, 8, 3>(a, st);
-        case 1: return launch_few<YT, 2, 1, 8, 2>(a, st);
-        case 2: return launch_few<YT, 2, 2, 8, 2>(a, st);
-        case 3: return launch_few<YT, 2, 2, 4, 2>(a, st);
-        case 4: return launch_few<YT, 4, 2, 8, 1>(a, st);
-        default: return launch_few<YT, 4, 4, 4, 1>(a, st);
+        case 0: return launch_few<YT, 1, 1, 4, 2>(a, st);
+        case 1: return launch_few<YT, 1, 2, 4, 1>(a, st);
+        case 2: return launch_few<YT, 2, 2, 4, 1>(a, st);
+        case 3: return launch_few<YT, 2, 3, 4, 1>(a, st);
+        default: return launch_few<YT, 3, 2, 4, 1>(a, st);
     }
 }
 
 }  // namespace
 
+// The tile expected to be fastest.  A CU takes in about 90 bytes a nanosecond
+// of the operands from L2, whatever the tile, so a tile of tg x ng row groups
+// costs 16 K (tg + ng) bytes of that, plus what its workgroups spend outside
+// their K loop (own), as often as the workgroups go round the CUs, plus a
+// start (us).  The 256x256 tiles are bound by the matrix cores instead.
+// Measured (us, with gate and residual) against the 256x256 tiles: 5120 ->
+// 13824 at 1, 64, 256, 384 tokens 8.3, 10.7, 24.5, 32.0 (33.4, 33.8, 35.6,
+// 37.6; from about 500 tokens on they win), 13824 -> 5120 at 1, 64, 256, 1024
+// tokens 8.4, 12.7, 22.2, 65.9 (72.9, 73.5, 74.8, 77.0), 1568 -> 1056 at 777
+// tokens 6.6 (19.6).
 int few_tile(int64_t M, int32_t N, int32_t K) {
-    // A CU takes in about 57 bytes a nanosecond, from L2 or beyond, whatever
-    // the tile: measured times follow the operand bytes of a workgroup times
-    // the workgroups per CU, plus what a workgroup spends outside its K loop.
-    static const struct { int tg, ng; double own; } tiles[] = {{1, 1, 1.0}, {2, 1, 1.5}, {2, 2, 2.0}, {2, 2, 2.0}, {4, 2, 3.0}, {4, 4, 10.0}};
-    const double cus = device_cu_count(), row = 16.0 * K / 57e3;      // us for 32 rows of K channels
-    const int64_t big = ((M + 255) / 256) * ((N + 255) / 256);
-    double best = (double)(int64_t)((big + cus - 1) / cus) * (16 * row + 8.0) + 4.0;
+    static const struct { int tg, ng; double start, own; } tiles[] = {
+        {1, 1, 3.2, 0.45}, {1, 2, 3.3, 0.9}, {2, 2, 6.2, 1.3}, {2, 3, 8.5, 1.5}, {3, 2, 8.5, 1.6}};
+    const double cus = device_cu_count();
+    const double big = (double)((M + 255) / 256) * (double)((N + 255) / 256);
+    double best = 10.0 + __builtin_ceil(big / cus) * (K * 0.00446 + 16.0 * (big < cus ? big / cus : 1.0));
     int tile = -1;
-    for (int i = 0; i < 6; ++i) {
-        const int64_t wgs = ((M + 32 * tiles[i].tg - 1) / (32 * tiles[i].tg)) * ((N + 32 * tiles[i].ng - 1) / (32 * tiles[i].ng));
-        if (i == 2 ? wgs > cus : i == 3 ? wgs <= cus : false) continue;   // 8 waves if alone on a CU, else two of 4
-        const double rounds = wgs > 2 * cus ? wgs / cus : wgs > cus ? 2.0 : 1.0;
-        const double t = rounds * ((tiles[i].tg + tiles[i].ng) * row + tiles[i].own);
+    for (int i = 0; i < 5; ++i) {
+        const int tg = tiles[i].tg, ng = tiles[i].ng;
+        const double wgs = (double)((M + 32 * tg - 1) / (32 * tg)) * (double)((N + 32 * ng - 1) / (32 * ng)), r = wgs / cus;
+        const double rounds = r <= 3.0 ? __builtin_ceil(r) : r + 0.3;
+        const double t = tiles[i].start + rounds * (16.0 * K * (tg + ng) / 90e3 + tiles[i].own);
         if (t < best) {
             best = t;
             tile = i;

@@ -533,15 +533,22 @@ struct QuantLane {
     float s[8], rz[8];
     uint32_t keep, lim;
 };
-__device__ __forceinline__ void quant_lane(const NormQuantArgs& g, int j0, bool in, QuantLane& q) {
-    bool ok = true;
-    q.keep = 0xFFFFFFFFu;
-    const int j = in ? j0 : 0;         // 32-byte pieces of the plan's vectors
+struct QuantRaw {                       // 32-byte pieces of the plan's vectors, loaded ahead of their use
+    float4 s0, s1, r0, r1;
+    int4 p0, p1;
+};
+__device__ __forceinline__ void quant_load(const NormQuantArgs& g, int j0, bool in, QuantRaw& q) {
+    const int j = in ? j0 : 0;
     const float4* ps = reinterpret_cast<const float4*>(g.s + j);
     const float4* pr = reinterpret_cast<const float4*>(g.rcp + j);
     const int4* pp = reinterpret_cast<const int4*>(g.pos + j);
-    const float4 s0 = ps[0], s1 = ps[1], r0 = pr[0], r1 = pr[1];
-    const int4 p0 = pp[0], p1 = pp[1];
+    q = QuantRaw{ps[0], ps[1], pr[0], pr[1], pp[0], pp[1]};
+}
+__device__ __forceinline__ void quant_make(const QuantRaw& w, bool in, QuantLane& q) {
+    bool ok = true;
+    q.keep = 0xFFFFFFFFu;
+    const float4 s0 = w.s0, s1 = w.s1, r0 = w.r0, r1 = w.r1;
+    const int4 p0 = w.p0, p1 = w.p1;
     const float s[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w}, r[8] = {r0.x, r0.y, r0.z, r0.w, r1.x, r1.y, r1.z, r1.w};
     const int p[8] = {p0.x, p0.y, p0.z, p0.w, p1.x, p1.y, p1.z, p1.w};
 #pragma unroll
@@ -553,6 +560,12 @@ __device__ __forceinline__ void quant_lane(const NormQuantArgs& g, int j0, bool 
         ok &= div_fast_ok_s(q.s[i]);
     }
     q.lim = ok ? kF32Pow126 : 0u;
+}
+
+__device__ __forceinline__ void quant_lane(const NormQuantArgs& g, int j0, bool in, QuantLane& q) {
+    QuantRaw w;
+    quant_load(g, j0, in, w);
+    quant_make(w, in, q);
 }
 
 // E2M1 codes (packed, first value in the low nibble) and E8M0 code of 8 bf16
@@ -744,6 +757,10 @@ norm_quant_kernel(NormQuantArgs g, int R) {
     };
     const int64_t step = (int64_t)gridDim.x * R;
     int64_t r0 = (int64_t)blockIdx.x * R;
+    if (r0 >= M) {                                                    // pad rows only
+        for (; r0 < Mp; r0 += step) flush_unit<0>(g, r0, 0, M32, ns4, nso, nwin, stage, rowA, stS, rowS, t.T, R);
+        return;
+    }
     if constexpr (KEEP) {
         load_row(r0);
 #pragma unroll
