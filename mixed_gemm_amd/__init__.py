@@ -940,3 +940,60 @@ def ffn_block_forward(blk: FFNBlock, X: torch.Tensor, stream=None, epilogue: boo
     y2 = torch.empty((X.shape[0], blk.plan2.desc.N), dtype=torch.bfloat16, device=X.device)
     mg_dual_gemm(blk.plan2, a2, y2, stream)
     return y2
+
+
+@dataclass
+class FFNSublayer:
+    """x + gate * (ffn.2(gelu(ffn.0(h) + bias0)) + bias2) with h = norm(x) (1 +
+    scale) + shift: the FFN block with the norm ahead of it, its biases and the
+    gated residual behind it."""
+    block: FFNBlock
+    norm: Norm
+    bias0: torch.Tensor | None = None
+    bias2: torch.Tensor | None = None
+
+
+@_on_stream
+def ffn_sublayer_stats(calib_batches, W0: torch.Tensor, norm: Norm, bias0: torch.Tensor | None = None, stream=None):
+    """Calibration statistics of a sublayer's two projections, from (x, mod)
+    batches of its input rows and their modulation: ffn.0's from h = norm(x)
+    (1 + scale) + shift, ffn.2's from the unquantized gelu(h W0^T + bias0).
+    Returns (act_max0, act_max2) for ffn_block_plans."""
+    N0, K0 = W0.shape
+    act0 = torch.empty(K0, dtype=torch.float32, device=W0.device)
+    act2 = torch.empty(N0, dtype=torch.float32, device=W0.device)
+    mg_calib_reset(act0, stream)
+    mg_calib_reset(act2, stream)
+    ref0 = reference_plan(W0, stream)
+    ep = Epilogue(bias0, "gelu")
+    for x, mod in calib_batches:
+        h = torch.empty((x.shape[0], K0), dtype=torch.bfloat16, device=x.device)
+        mg_norm_mod(norm, mod, x, h, stream)
+        mg_calib_act(h, act0, stream)
+        y = torch.empty((x.shape[0], N0), dtype=torch.bfloat16, device=x.device)
+        mg_forward_ep(ref0, h, Act.empty(ref0.desc, x.shape[0], x.device), ep, y, stream)
+        mg_calib_act(y, act2, stream)
+    return act0, act2
+
+
+@_on_stream
+def ffn_sublayer_forward(sub: FFNSublayer, x: torch.Tensor, mod: Mod, attn: torch.Tensor | None = None,
+                         attn_gate: Mod | None = None, stream=None) -> torch.Tensor:
+    """One step of the sublayer on the residual stream x [M][K] (float32 or
+    bf16; a new tensor of its type is returned).  mod holds shift, scale and
+    gate.  With attn, the output of the attention block before it, the stream
+    is first advanced to x + attn_gate * attn."""
+    p0, p2 = sub.block.plan0, sub.block.plan2
+    M = x.shape[0]
+    if attn is not None:
+        x1 = torch.empty((M, p0.desc.K), dtype=x.dtype, device=x.device)
+        mg_residual_norm(x, attn, x1, attn_gate, stream=stream)
+        x = x1
+    a0, a2 = Act.empty(p0.desc, M, x.device), Act.empty(p2.desc, M, x.device)
+    y0 = torch.empty((M, p0.desc.N), dtype=torch.bfloat16, device=x.device)
+    mg_norm_quantize_act(p0, sub.norm, mod, x, a0, stream)
+    mg_dual_gemm_ep(p0, a0, Epilogue(sub.bias0), y0, stream)
+    mg_gelu_quantize_act(p2, y0, a2, stream)
+    out = torch.empty((M, p2.desc.N), dtype=x.dtype, device=x.device)
+    mg_dual_gemm_ep(p2, a2, Epilogue(sub.bias2, gate=mod, residual=x), out, stream)
+    return out

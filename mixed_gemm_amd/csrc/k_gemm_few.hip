@@ -71,7 +71,7 @@ __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW
     constexpr int ROW = 32 * NG + 4;                                  // floats per staged row
     constexpr int PR = 8 * NG;                                        // pieces of 4 columns per token
     constexpr int RS = 64 * NW / PR;                                  // token rows the workgroup takes at once
-    constexpr int PT = RS >= 32 ? 1 : 32 / RS;                        // pieces per thread and token group
+    constexpr int PT = (32 + RS - 1) / RS;                            // pieces per thread and token group
     constexpr bool EARLY = TG == 1 && PT == 1;                        // epilogue inputs loaded ahead of the K loop
     const int tid = threadIdx.x, lane = tid & 63, l32 = lane & 31, h = lane >> 5;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -89,14 +89,14 @@ __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW
 
     // ---- the epilogue's inputs: a thread's columns are the same in every row it takes
     const int prow = tid / PR, pcol = n0 + 4 * (tid % PR);
-    const bool pon = prow < 32 && pcol < N;
+    const bool pon = prow < (RS < 32 ? RS : 32) && pcol < N;
     float bias[4] = {}, gate[PT][4], res[PT][4];
     int mi[PT];
     auto ep_inputs = [&](int t) {
 #pragma unroll
         for (int p = 0; p < PT; ++p) {
             const int64_t m = t0 + 32 * t + p * RS + prow;
-            const bool on = pon && m < M;
+            const bool on = pon && p * RS + prow < 32 && m < M;
             mi[p] = on ? mod_row(e.mod, m) : -1;
 #pragma unroll
             for (int c = 0; c < 4; ++c) { gate[p][c] = 1.0f; res[p][c] = 0.0f; }
@@ -241,7 +241,7 @@ __global__ void __launch_bounds__(64 * NW) __attribute__((amdgpu_waves_per_eu(NW
 #pragma unroll
         for (int p = 0; p < PT; ++p) {
             const int64_t m = t0 + 32 * t + p * RS + prow;
-            if (!pon || m >= M) continue;
+            if (!pon || p * RS + prow >= 32 || m >= M) continue;
             float v[4] = {};
 #pragma unroll
             for (int x = 0; x < NW; ++x) {
@@ -285,8 +285,7 @@ hipError_t run_few(int tile, const FewArgs& a, hipStream_t st) {
         case 0: return launch_few<YT, 1, 1, 4, 2>(a, st);
         case 1: return launch_few<YT, 1, 2, 4, 1>(a, st);
         case 2: return launch_few<YT, 2, 2, 4, 1>(a, st);
-        case 3: return launch_few<YT, 2, 3, 4, 1>(a, st);
-        default: return launch_few<YT, 3, 2, 4, 1>(a, st);
+        default: return launch_few<YT, 2, 3, 4, 1>(a, st);
     }
 }
 
@@ -300,16 +299,16 @@ hipError_t run_few(int tile, const FewArgs& a, hipStream_t st) {
 // Measured (us, with gate and residual) against the 256x256 tiles: 5120 ->
 // 13824 at 1, 64, 256, 384 tokens 8.3, 10.7, 24.5, 32.0 (33.4, 33.8, 35.6,
 // 37.6; from about 500 tokens on they win), 13824 -> 5120 at 1, 64, 256, 1024
-// tokens 8.4, 12.7, 22.2, 65.9 (72.9, 73.5, 74.8, 77.0), 1568 -> 1056 at 777
+// tokens 8.4, 12.7, 22.9, 67.9 (72.9, 73.5, 74.8, 77.0), 1568 -> 1056 at 777
 // tokens 6.6 (19.6).
 int few_tile(int64_t M, int32_t N, int32_t K) {
     static const struct { int tg, ng; double start, own; } tiles[] = {
-        {1, 1, 3.2, 0.45}, {1, 2, 3.3, 0.9}, {2, 2, 6.2, 1.3}, {2, 3, 8.5, 1.5}, {3, 2, 8.5, 1.6}};
+        {1, 1, 3.2, 0.45}, {1, 2, 3.3, 0.9}, {2, 2, 6.2, 1.3}, {2, 3, 8.5, 1.5}};
     const double cus = device_cu_count();
     const double big = (double)((M + 255) / 256) * (double)((N + 255) / 256);
     double best = 10.0 + __builtin_ceil(big / cus) * (K * 0.00446 + 16.0 * (big < cus ? big / cus : 1.0));
     int tile = -1;
-    for (int i = 0; i < 5; ++i) {
+    for (int i = 0; i < 4; ++i) {
         const int tg = tiles[i].tg, ng = tiles[i].ng;
         const double wgs = (double)((M + 32 * tg - 1) / (32 * tg)) * (double)((N + 32 * ng - 1) / (32 * ng)), r = wgs / cus;
         const double rounds = r <= 3.0 ? __builtin_ceil(r) : r + 0.3;

@@ -354,12 +354,12 @@ def decoded(p, a, M):
     d = p.desc
     A = mxfp4.decode_rows(aq_rows(a.Aq, M, d.K), scale_rows(a.As, M, d.K)).astype(np.float64)
     W = mxfp4.decode_rows(aq_rows(p.Wq, d.N, d.K), scale_rows(p.Ws, d.N, d.K)).astype(np.float64)
-    v, t = A @ W.T, np.abs(A) @ np.abs(W).T
     if d.k:
         from tests.gpu_util import bf16_to_f64
-        x, w = bf16_to_f64(outlier_cols(a.XO, M, d.k)), bf16_to_f64(outlier_cols(p.WO, d.N, d.k))
-        v, t = v + x @ w.T, t + np.abs(x) @ np.abs(w).T
-    return v, t
+        A = np.concatenate([A, bf16_to_f64(outlier_cols(a.XO, M, d.k))], axis=1)
+        W = np.concatenate([W, bf16_to_f64(outlier_cols(p.WO, d.N, d.k))], axis=1)
+    A, W = torch.from_numpy(A).cuda(), torch.from_numpy(W).cuda()
+    return f64(A @ W.t()), f64(A.abs() @ W.abs().t())
 
 
 EP_CASES = [
@@ -375,6 +375,15 @@ EP_CASES = [
     (300, 1056, 1312, 64, "bf16", "bf16", "silu", True, "bf16", "sample", "f32"),
     (777, 1568, 1056, 40, "f32", "bf16", "none", True, "f32", "token", "f32"),
     (1100, 640, 288, 16, "f32", None, "gelu", False, "bf16", "sample", "f32"),
+    # larger tiles of the few-token form, ragged in both directions, and the 256x256 tiles
+    (100, 4128, 4000, 40, "bf16", "f32", "none", True, "bf16", "token", "f32"),
+    (515, 4128, 4000, 40, "f32", "bf16", "silu", True, "f32", "sample", "bf16"),
+    (1010, 4128, 4000, 96, "bf16", "f32", "gelu", True, "f32", "token", "f32"),
+    (2100, 4128, 4000, 5, "bf16", "bf16", "gelu", False, None, "sample", "f32"),
+    (2100, 2080, 4000, 33, "f32", "bf16", "none", True, "f32", "sample", "f32"),
+    (2050, 2080, 4000, 0, "bf16", "f32", "silu", True, "bf16", "token", "bf16"),
+    (2305, 1056, 4000, 17, "f32", None, "none", False, "f32", "sample", "f32"),
+    (2560, 1056, 4000, 17, "bf16", "f32", "none", False, "f32", "token", "f32"),
 ]
 
 
@@ -416,6 +425,41 @@ def test_gemm_epilogue(M, K, N, k, yt, bias, act, gate, res, mod, mt):
         Y2.fill_(float("nan"))
         mg.mg_dual_gemm_ep(p, a, mg.Epilogue(b, act, g, R), Y2)
         assert torch.equal(Y[:M], Y2), "the same call gives the same bits"
+
+
+@pytest.mark.parametrize("act", ["none", "gelu", "silu"])
+@pytest.mark.parametrize("yt", ["bf16", "f32"])
+@pytest.mark.parametrize("res", [None, "bf16", "f32"])
+def test_every_form_of_the_large_tiles_epilogue(act, yt, res):
+    """Shapes that take the 256x256 tiles; each activation, output and residual
+    type, with one gate row, one per token, and none."""
+    M, K, N = 5000, 512, 2048
+    rng = np.random.default_rng(len(act) + 10 * len(yt))
+    X, _ = rows(rng, M, K, "bf16")
+    p = _quant_plan(rng, K, N, 7, X)
+    a = mg.Act.empty(p.desc, M)
+    mg.mg_quantize_act(p, X, a)
+    v, t = decoded(p, a, M)
+    b = vec(rng, N, "f32")
+    ga = modulation(rng, 3, N, "f32")[2]
+    R = rows(rng, M, N, res)[0] if res else None
+    z = v + f64(b)
+    dv = (K + 9) * U * t + U * (np.abs(v) + np.abs(f64(b)))
+    av = block.activation(z, act)
+    if act != "none":
+        e = np.abs(z) * 1.4427 if act == "silu" else np.abs(2.3022 * z + 0.10295 * z ** 3)
+        dv = 1.13 * dv + np.abs(av) * (12 + 4 * e) * U + 1e-37
+    for mode in ("none", "sample", "token"):
+        i, g = np.zeros(M, int), None
+        if mode != "none":
+            where, i = _where(rng, mode, M, 3)
+            g = mg.Mod(gate=ga, **where)
+        Y = torch.full((M, N), float("nan"), dtype=TYPES[yt], device="cuda")
+        mg.mg_dual_gemm_ep(p, a, mg.Epilogue(b, act, g, R), Y)
+        ref = block.gated(np.zeros_like(v) if R is None else f64(R), av, i, f64(ga) if g else None)
+        gg = np.abs(f64(ga)[np.maximum(i, 0)]) if g else 1.0
+        dy = np.where((i < 0)[:, None], 0.0, gg * dv + 3 * U * gg * np.abs(av)) + U * np.abs(ref) + 1e-37
+        assert_close(f64(Y), ref, dy, yt, mode)
 
 
 def test_epilogue_in_place_on_the_residual():
@@ -503,6 +547,74 @@ def test_replayed_in_a_graph():
         step()
         torch.cuda.synchronize()
         assert torch.equal(got, O), seed
+
+
+# ------------------------------------------------------- the path end to end
+
+@pytest.mark.parametrize("M,dt", [(1, "bf16"), (40, "f32"), (700, "bf16"), (2600, "f32")])
+def test_ffn_sublayer_on_unquantized_plans(M, dt):
+    """The whole path -- attention residual, norm, both projections with biases,
+    gate and residual -- on plans that keep every channel in bf16, against
+    float64.  Each rounding to bf16 on the way (h, ffn.0's output, its GELU) is
+    at most 2^-8 of its value and passes through the weights in absolute value;
+    a value's f32 error is far below one such rounding, which is counted twice."""
+    rng = np.random.default_rng(M)
+    K, N = 256, 512
+    x, _ = rows(rng, M, K, dt)
+    attn, _ = rows(rng, M, K, "bf16")
+    W0, W2 = (torch.from_numpy(rng.standard_normal(s) * 0.05).cuda().bfloat16() for s in ((N, K), (K, N)))
+    b0, b2 = vec(rng, N, "bf16"), vec(rng, K, "f32")
+    sc, sh, ga = modulation(rng, 2, K, "f32")
+    where, i = _where(rng, "token" if M > 40 else "sample", M, 2)
+    m = mg.Mod(scale=sc, shift=sh, gate=ga, **where)
+    sub = mg.FFNSublayer(mg.FFNBlock(mg.reference_plan(W0), mg.reference_plan(W2)), mg.Norm(), b0, b2)
+    out = mg.ffn_sublayer_forward(sub, x, m, attn, m)
+    r = 2.0 ** -8
+    x1 = block.gated(f64(x), f64(attn), i, f64(ga))
+    dx = np.abs(x1) * (r if dt == "bf16" else 4 * U) + 1e-37
+    h = block.modulate(block.norm(x1), i, f64(sc), f64(sh))
+    rstd = 1 / np.sqrt(x1.var(axis=1, keepdims=True) + 1e-6)
+    k = np.maximum(i, 0)
+    n = np.abs(block.norm(x1))
+    dh = np.abs(1 + f64(sc)[k]) * rstd * (dx + dx.mean(axis=1, keepdims=True) + n * np.sqrt((dx ** 2).mean(axis=1, keepdims=True)))
+    dh = np.where((i < 0)[:, None], 0.0, dh * (1 + 4 * r) + 2 * r * np.abs(h))
+    y = h @ f64(W0).T + f64(b0)
+    dy = dh @ np.abs(f64(W0)).T + 2 * r * np.abs(y) + 1e-6
+    g = block.activation(y, "gelu")
+    dg = 1.13 * dy + 2 * r * np.abs(g) + 2.0 ** -24
+    v = g @ f64(W2).T + f64(b2)
+    dv = dg @ np.abs(f64(W2)).T + 1e-6
+    ref = block.gated(x1, v, i, f64(ga))
+    bound = dx + np.where((i < 0)[:, None], 0.0, np.abs(f64(ga)[k]) * dv * (1 + r)) + 4 * U * np.abs(ref)
+    assert_close(f64(out), ref, bound, dt, "out")
+    assert out.dtype == x.dtype
+
+
+def test_ffn_sublayer_quantized():
+    """Calibrated W4A4 plans: the path is its public steps, bit for bit, and the statistics are the steps'."""
+    rng = np.random.default_rng(77)
+    K, N, M = 512, 1024, 300
+    W0, W2 = (torch.from_numpy(rng.standard_normal(s) * 0.03).cuda().bfloat16() for s in ((N, K), (K, N)))
+    b0, b2 = vec(rng, N, "f32"), vec(rng, K, "bf16")
+    sc, sh, ga = modulation(rng, 1, K, "bf16")
+    m, norm = mg.Mod(scale=sc, shift=sh, gate=ga), mg.Norm("rms", vec(rng, K, "bf16", 1.0))
+    xs = [rows(rng, M, K, "f32")[0] for _ in range(3)]
+    act0, act2 = mg.ffn_sublayer_stats([(x, m) for x in xs], W0, norm, b0)
+    hs = [torch.empty(M, K, dtype=torch.bfloat16, device="cuda") for _ in xs]
+    for x, h in zip(xs, hs):
+        mg.mg_norm_mod(norm, m, x, h)
+    assert torch.equal(act0, torch.stack([h.abs().amax(0) for h in hs]).amax(0).float())
+    blk = mg.ffn_block_plans(act0, act2, W0, W2, 0.6, 8, 0.5, 16)
+    out = mg.ffn_sublayer_forward(mg.FFNSublayer(blk, norm, b0, b2), xs[0], m)
+    a0, a2 = mg.Act.empty(blk.plan0.desc, M), mg.Act.empty(blk.plan2.desc, M)
+    y0, want = torch.empty(M, N, dtype=torch.bfloat16, device="cuda"), torch.empty_like(xs[0])
+    mg.mg_forward_ep(blk.plan0, hs[0], a0, mg.Epilogue(b0), y0)
+    mg.mg_gelu_quantize_act(blk.plan2, y0, a2)
+    mg.mg_dual_gemm_ep(blk.plan2, a2, mg.Epilogue(b2, gate=m, residual=xs[0]), want)
+    assert torch.equal(out, want)
+    y = torch.nn.functional.gelu(hs[0].double() @ W0.double().t() + b0.double(), approximate="tanh")
+    ref = xs[0].double() + ga.double() * (y @ W2.double().t() + b2.double())
+    assert ((out - ref).norm() / (ref - xs[0]).norm()).item() < 0.5     # 4 bits: a coarse check of the wiring
 
 
 # ------------------------------------------------------------------ refusals
