@@ -12,8 +12,9 @@
 // through LDS serves both.
 //
 // Rows may start at any element and have any width from 8 on: loads are
-// unaligned 16-byte loads, and a thread at the row's end loads the row's last
-// 8 channels and shifts them into place, so that no load needs a branch.
+// unaligned 16-byte loads, and a thread at the row's end holds the row's last
+// 8 channels, so that no load needs a branch; those of them that the thread
+// before holds too count as 0 in the sums and are not stored.
 #include <type_traits>
 
 #include "mg_block.h"
@@ -107,7 +108,7 @@ template <int V, bool ODD = true>
 struct RowThread {
     int W, T, wave, K, shift;       // shift: channels missing in the row's last vector
     int col[V];                     // first channel of vector v
-    int at[V];                      // where its 8 elements are loaded from (the row's last 8 past col = K - 8)
+    int at[V];                      // channel of its first element (past K - 8: K - 8, the row's last 8)
     uint32_t full, cut;             // bit v: the wave's vector lies inside the row; holds its last, partial vector
     float rn, rK;                   // 1 / channels of this wave, 1 / K
     float nl, rnl;                  // channels of wave (lane % 16), 1 / them (0 past the last wave)
@@ -141,17 +142,21 @@ struct RowThread {
         rnl = cl ? 1.0f / (float)cl : 0.0f;
         rK = 1.0f / (float)K;
     }
-    __device__ __forceinline__ int left(int v) const { return K - col[v]; }
+    // Of a vector's 8 elements the first skip(v) are not its own: 0 inside the
+    // row, 8 or more past it.  In the row's last, partial vector they are the
+    // vector before's: counted nowhere and never stored.
+    __device__ __forceinline__ int skip(int v) const { return col[v] - at[v]; }
     __device__ __forceinline__ bool whole() const { return full == (1u << V) - 1u; }
-    // Values loaded at at[v] moved to the vector's own channels (those past the
-    // row hold anything: they are counted nowhere and never stored).
-    __device__ __forceinline__ void place(int v, float (&x)[8]) const {
+    // 0 in elements that are not the vector's own
+    __device__ __forceinline__ void own(int v, float (&x)[8]) const {
+        if (full >> v & 1u) return;
         if (ODD && (cut >> v & 1u)) {
-            const bool me = col[v] < K && col[v] > K - 8;
-            for (int k = 0; k < shift; ++k) {
 #pragma unroll
-                for (int i = 0; i < 7; ++i) x[i] = me ? x[i + 1] : x[i];
-            }
+            for (int i = 0; i < 8; ++i) x[i] = i >= skip(v) ? x[i] : 0.0f;
+        } else {
+            const bool in = skip(v) == 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = in ? x[i] : 0.0f;
         }
     }
     // 8 values of a [K] array of either type
@@ -159,12 +164,11 @@ struct RowThread {
         RawAny r;
         load_any(p, row + at[v], dtype, r);
         unpack(r, dtype, x);
-        place(v, x);
     }
     __device__ __forceinline__ void store8(void* p, int64_t row, int32_t dtype, int v, const float (&x)[8]) const {
         const bool f32 = dtype == MG_F32;
-        float* const pf = static_cast<float*>(p) + row + col[v];
-        uint16_t* const pb = static_cast<uint16_t*>(p) + row + col[v];
+        float* const pf = static_cast<float*>(p) + row + at[v];
+        uint16_t* const pb = static_cast<uint16_t*>(p) + row + at[v];
         auto piece = [&]() {
             if (f32) {
                 u32x4 a, b;
@@ -178,14 +182,14 @@ struct RowThread {
         };
         if (full >> v & 1u) {
             piece();
-        } else if (left(v) >= 8) {
-            piece();
-        } else {
-            const int l = left(v);
+            return;
+        }
+        if (skip(v) == 0) piece();
+        if (ODD && (cut >> v & 1u) && skip(v) == shift) {
             const u32x4 w = pack8_bf16(x);
 #pragma unroll
-            for (int i = 0; i < 7; ++i)
-                if (i < l) {
+            for (int i = 1; i < 8; ++i)
+                if (i >= shift) {
                     if (f32) pf[i] = x[i];
                     else pb[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
                 }
@@ -213,15 +217,15 @@ __device__ __forceinline__ void row_stats(const float (&x)[V][8], const RowThrea
                                           int& turn, float& mean, float& rstd) {
     float s = 0.0f, m = 0.0f, q = 0.0f;
     const bool layer = kind == MG_NORM_LAYER;
+    if (layer) {                                        // what is not the vector's own is 0
+#pragma unroll
+        for (int v = 0; v < V; ++v)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s += x[v][i];
+        s = wave_sum(s);
+        m = s * t.rn;
+    }
     if (t.whole()) {
-        if (layer) {
-#pragma unroll
-            for (int v = 0; v < V; ++v)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) s += x[v][i];
-            s = wave_sum(s);
-            m = s * t.rn;
-        }
 #pragma unroll
         for (int v = 0; v < V; ++v)
 #pragma unroll
@@ -229,20 +233,22 @@ __device__ __forceinline__ void row_stats(const float (&x)[V][8], const RowThrea
                 const float d = x[v][i] - m;
                 q = __builtin_fmaf(d, d, q);
             }
-    } else {
-        if (layer) {
+    } else if (!ODD || !t.cut) {
 #pragma unroll
-            for (int v = 0; v < V; ++v)
+        for (int v = 0; v < V; ++v) {
+            const float mv = t.skip(v) == 0 ? m : 0.0f;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) s += i < t.left(v) ? x[v][i] : 0.0f;
-            s = wave_sum(s);
-            m = s * t.rn;
+            for (int i = 0; i < 8; ++i) {
+                const float d = x[v][i] - mv;
+                q = __builtin_fmaf(d, d, q);
+            }
         }
+    } else {
 #pragma unroll
         for (int v = 0; v < V; ++v)
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float d = i < t.left(v) ? x[v][i] - m : 0.0f;
+                const float d = i >= t.skip(v) ? x[v][i] - m : 0.0f;
                 q = __builtin_fmaf(d, d, q);
             }
     }
@@ -293,8 +299,6 @@ __device__ __forceinline__ void fold_make(const RowThread<V, ODD>& t, const Norm
 #pragma unroll
         for (int i = 0; i < 8; ++i) a[i] *= w[i];
     }
-    t.place(v, a);
-    t.place(v, c);
 }
 template <int V, bool ODD>
 __device__ __forceinline__ void fold8(const RowThread<V, ODD>& t, const NormArgs& n, const ModArgs& m, int row, int v,
@@ -323,26 +327,52 @@ __device__ __forceinline__ void apply8(float (&x)[8], float mean, float rstd, co
 #pragma unroll
     for (int i = 0; i < 8; ++i) x[i] = __builtin_fmaf(__builtin_fmaf(x[i], rstd, b), a[i], c[i]);
 }
-// The norm after the block (weight pw; the rare bias is read where it is used).
-template <int V>
-__device__ __forceinline__ void post8(const RowThread<V>& t, float (&y)[8], const NormArgs& n, const float (&pw)[8], int v,
-                                      float mean, float rstd) {
-    const float b = -mean * rstd;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = __builtin_fmaf(y[i], rstd, b) * pw[i];
-    if (n.bias) {
-        float c[8];
-        t.load8(n.bias, 0, n.dtype, v, c);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) y[i] += c[i];
-    }
-}
 // 8 values of an optional array (1 without one)
 template <int V>
 __device__ __forceinline__ void load_or_1(const RowThread<V>& t, const void* p, int64_t row, int32_t dtype, int v, float (&g)[8]) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) g[i] = 1.0f;
     if (p) t.load8(p, row, dtype, v, g);
+}
+
+// Arguments that a row rarely needs, read from the kernel-argument segment
+// (which starts with a RowArgs) where they are used, through a pointer the
+// compiler cannot see through: held in scalar registers across the rows they
+// would be spilled there.
+typedef const __attribute__((address_space(4))) RowArgs* RowKernargs;
+__device__ __forceinline__ RowKernargs row_kernargs() {
+    RowKernargs p = (RowKernargs)__builtin_amdgcn_kernarg_segment_ptr();
+    asm volatile("" : "+s"(p));
+    return p;
+}
+__device__ __forceinline__ NormArgs norm_of(const __attribute__((address_space(4))) NormArgs& n) {
+    return NormArgs{n.weight, n.bias, n.dtype, n.kind, n.eps};
+}
+__device__ __forceinline__ ModArgs mod_of(const __attribute__((address_space(4))) ModArgs& m) {
+    return ModArgs{m.scale, m.shift, m.gate, m.index, m.ld, m.group, m.rows, m.dtype};
+}
+struct FoldArgs {
+    NormArgs norm;
+    ModArgs mod;
+};
+__device__ __forceinline__ FoldArgs fold_args() {
+    const RowKernargs p = row_kernargs();
+    return FoldArgs{norm_of(p->norm), mod_of(p->mod)};
+}
+
+// The norm after the block (weight pw; the rare bias is read where it is used).
+template <int V>
+__device__ __forceinline__ void post8(const RowThread<V>& t, float (&y)[8], const float (&pw)[8], int v, float mean, float rstd) {
+    const float b = -mean * rstd;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = __builtin_fmaf(y[i], rstd, b) * pw[i];
+    const RowKernargs p = row_kernargs();
+    if (p->post.bias) {
+        float c[8];
+        t.load8(p->post.bias, 0, p->post.dtype, v, c);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) y[i] += c[i];
+    }
 }
 
 // The rows of a workgroup, r0 + i step for i < count: consecutive where token
@@ -372,53 +402,59 @@ row_kernel(RowArgs a, RowSpan span) {
     __shared__ Pairs pairs;
     int turn = 0;
     const RowThread<V> t(a.K);
-    const XT* X = static_cast<const XT*>(a.X);
-    const Y* Yp = static_cast<const Y*>(a.Y);
     float na[KEEP ? V : 1][8], nc[KEEP ? V : 1][8], ga[KEEP && RES ? V : 1][8], pw[KEEP && RES ? V : 1][8];
     int mi_of = -1, gi_of = -1;       // modulation rows that the kept coefficients belong to
     Raw8<XT> rx[V];
     Raw8<Y> ry[RES ? V : 1];
     int mrow = -1, grow = -1;         // modulation rows of the row ahead
-    int64_t r = span.step == 1 ? blockIdx.x * span.chunk : blockIdx.x;
-    const int64_t last = span.step == 1 ? (r + span.chunk < a.M ? r + span.chunk : a.M) - 1 : a.M - 1;
-    auto load_row = [&](int64_t r) {
+    const bool norm = !RES || a.has_norm, post = RES && a.has_post;
+    int64_t left = span.step == 1 ? a.M - blockIdx.x * span.chunk : (a.M - 1 - blockIdx.x) / span.step + 1;    // rows to do
+    if (span.step == 1 && left > span.chunk) left = span.chunk;
+    uint32_t r = (uint32_t)(span.step == 1 ? blockIdx.x * span.chunk : blockIdx.x);      // the row ahead (M < 2^31)
+    const XT* px = static_cast<const XT*>(a.X) + r * a.ldx;        // its rows of X and Y
+    const Y* py = static_cast<const Y*>(a.Y) + (RES ? r * a.ldy : 0);
+    int64_t oo = r * a.ldo, oh = r * a.ldh;                        // this row's of O and H
+    const int64_t sx = span.step * a.ldx, sy = span.step * a.ldy, so = span.step * a.ldo, sh = span.step * a.ldh;
+    auto load_row = [&]() {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
-            load_raw(X + r * a.ldx + t.at[v], rx[v]);
-            if constexpr (RES) load_raw(Yp + r * a.ldy + t.at[v], ry[v]);
+            load_raw(px + t.at[v], rx[v]);
+            if constexpr (RES) load_raw(py + t.at[v], ry[v]);
         }
-        if (!RES || a.has_norm) mrow = mod_row(a.mod, r);
+        if (norm) mrow = mod_row(a.mod, r);
         if constexpr (RES) grow = mod_row(a.gate, r);
     };
     if constexpr (KEEP && RES) {
-        if (a.has_post) {
+        if (post) {
 #pragma unroll
             for (int v = 0; v < V; ++v) load_or_1(t, a.post.weight, 0, a.post.dtype, v, pw[v]);
         }
     }
-    load_row(r);
+    load_row();
     while (true) {
         const int mi = __builtin_amdgcn_readfirstlane(mrow), gi = __builtin_amdgcn_readfirstlane(grow);
         if constexpr (KEEP) {
             const bool ng = RES && gi >= 0 && gi != gi_of;
-            RawAny rg[V];
-            if (ng) {
+            if (ng || (mi >= 0 && mi != mi_of)) {
+                RawAny rg[V];
+                ModArgs gm{};
+                if (ng) {
+                    gm = mod_of(row_kernargs()->gate);
 #pragma unroll
-                for (int v = 0; v < V; ++v) load_any(a.gate.gate, gi * a.gate.ld + t.at[v], a.gate.dtype, rg[v]);
-                gi_of = gi;
-            }
-            if (mi >= 0 && mi != mi_of) {
-                fold_all(t, a.norm, a.mod, mi, na, nc);
-                mi_of = mi;
-            }
-            if (ng) {
+                    for (int v = 0; v < V; ++v) load_any(gm.gate, gi * gm.ld + t.at[v], gm.dtype, rg[v]);
+                    gi_of = gi;
+                }
+                if (mi >= 0 && mi != mi_of) {
+                    const FoldArgs f = fold_args();
+                    fold_all(t, f.norm, f.mod, mi, na, nc);
+                    mi_of = mi;
+                }
+                if (ng) {
 #pragma unroll
-                for (int v = 0; v < V; ++v) {
+                    for (int v = 0; v < V; ++v) {
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) ga[RES ? v : 0][i] = 1.0f;
-                    if (a.gate.gate) {
-                        unpack(rg[v], a.gate.dtype, ga[RES ? v : 0]);
-                        t.place(v, ga[RES ? v : 0]);
+                        for (int i = 0; i < 8; ++i) ga[RES ? v : 0][i] = 1.0f;
+                        if (gm.gate) unpack(rg[v], gm.dtype, ga[RES ? v : 0]);
                     }
                 }
             }
@@ -427,50 +463,64 @@ row_kernel(RowArgs a, RowSpan span) {
 #pragma unroll
         for (int v = 0; v < V; ++v) {
             unpack(rx[v], x[v]);
-            t.place(v, x[v]);
+            t.own(v, x[v]);
             if constexpr (RES) {
                 unpack(ry[v], y[v]);
-                t.place(v, y[v]);
+                t.own(v, y[v]);
             }
         }
-        const int64_t next = r + span.step;
+        const bool more = --left > 0;
         // past the last row it is loaded once more, without a branch
-        if constexpr (S::ahead) load_row(next <= last ? next : last);
+        px += more ? sx : 0;
+        if constexpr (RES) py += more ? sy : 0;
+        r += more ? (uint32_t)span.step : 0u;
+        if constexpr (S::ahead) load_row();
         if constexpr (RES) {
             float mean = 0.0f, rstd = 1.0f;
-            if (a.has_post) row_stats(y, t, a.post.kind, a.post.eps, pairs, turn, mean, rstd);
+            if (post) row_stats(y, t, a.post.kind, a.post.eps, pairs, turn, mean, rstd);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 if (gi >= 0) {
-                    if (a.has_post) {
-                        if constexpr (!KEEP) load_or_1(t, a.post.weight, 0, a.post.dtype, v, pw[0]);
-                        post8(t, y[v], a.post, pw[KEEP ? v : 0], v, mean, rstd);
+                    if (post) {
+                        if constexpr (!KEEP) {
+                            const NormArgs n = norm_of(row_kernargs()->post);
+                            load_or_1(t, n.weight, 0, n.dtype, v, pw[0]);
+                        }
+                        post8(t, y[v], pw[KEEP ? v : 0], v, mean, rstd);
                     }
-                    if constexpr (!KEEP) load_or_1(t, a.gate.gate, gi * a.gate.ld, a.gate.dtype, v, ga[0]);
+                    if constexpr (!KEEP) {
+                        const ModArgs m = mod_of(row_kernargs()->gate);
+                        load_or_1(t, m.gate, gi * m.ld, m.dtype, v, ga[0]);
+                    }
 #pragma unroll
                     for (int i = 0; i < 8; ++i) x[v][i] = __builtin_fmaf(ga[KEEP ? v : 0][i], y[v][i], x[v][i]);
+                    t.own(v, x[v]);
                 }
-                t.store8(a.O, r * a.ldo, a.x_dtype, v, x[v]);
+                t.store8(a.O, oo, sizeof(XT) == 4 ? MG_F32 : MG_BF16, v, x[v]);
             }
+            oo += so;
         }
-        if (!RES || a.has_norm) {
+        if (norm) {
             float mean, rstd;
             row_stats(x, t, a.norm.kind, a.norm.eps, pairs, turn, mean, rstd);
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 if (mi >= 0) {
-                    if constexpr (!KEEP) fold8(t, a.norm, a.mod, mi, v, na[0], nc[0]);
+                    if constexpr (!KEEP) {
+                        const FoldArgs f = fold_args();
+                        fold8(t, f.norm, f.mod, mi, v, na[0], nc[0]);
+                    }
                     apply8(x[v], mean, rstd, na[KEEP ? v : 0], nc[KEEP ? v : 0]);
                 } else {
 #pragma unroll
                     for (int i = 0; i < 8; ++i) x[v][i] = 0.0f;
                 }
-                t.store8(a.H, r * a.ldh, a.h_dtype, v, x[v]);
+                t.store8(a.H, oh, a.h_dtype, v, x[v]);
             }
+            oh += sh;
         }
-        r = next;
-        if (r > last) break;
-        if constexpr (!S::ahead) load_row(r);
+        if (!more) break;
+        if constexpr (!S::ahead) load_row();
     }
 }
 
@@ -620,35 +670,6 @@ __device__ __forceinline__ uint32_t quant8(const float (&s)[8], const float (&rz
     return word & keep;
 }
 
-// The norm's and the modulation's arguments, read from the kernel-argument
-// segment (whose start is the kernel's first parameter) where they are used,
-// through a pointer the compiler cannot see through: held in scalar registers
-// across the rows they would be spilled there.
-struct FoldArgs {
-    NormArgs norm;
-    ModArgs mod;
-};
-__device__ __forceinline__ FoldArgs fold_args() {
-    typedef const __attribute__((address_space(4))) NormQuantArgs* KernargPtr;
-    KernargPtr p = (KernargPtr)__builtin_amdgcn_kernarg_segment_ptr();
-    asm volatile("" : "+s"(p));
-    FoldArgs f;
-    f.norm.weight = p->r.norm.weight;
-    f.norm.bias = p->r.norm.bias;
-    f.norm.dtype = p->r.norm.dtype;
-    f.norm.kind = p->r.norm.kind;
-    f.norm.eps = p->r.norm.eps;
-    f.mod.scale = p->r.mod.scale;
-    f.mod.shift = p->r.mod.shift;
-    f.mod.gate = nullptr;
-    f.mod.index = nullptr;
-    f.mod.ld = p->r.mod.ld;
-    f.mod.group = 1;
-    f.mod.rows = p->r.mod.rows;
-    f.mod.dtype = p->r.mod.dtype;
-    return f;
-}
-
 // Outlier columns are formed apart from the bulk, a lane per column of XO: its
 // channel's value is read again (the row has just been loaded), normed,
 // rounded and divided like every other's, so 64 of them cost one wave some 40
@@ -781,7 +802,10 @@ norm_quant_kernel(NormQuantArgs g, int R) {
             }
             float x[V][8];
 #pragma unroll
-            for (int v = 0; v < V; ++v) unpack(rx[v], x[v]);
+            for (int v = 0; v < V; ++v) {
+                unpack(rx[v], x[v]);
+                t.own(v, x[v]);
+            }
             const float xo0 = outlier_x(X + r * a.ldx, ol);
             if constexpr (KEEP) load_row(rr + 1 < live ? r + 1 : r0 + step);
             float mean, rstd;
@@ -1156,8 +1180,12 @@ hipError_t launch_rows(const RowArgs& a, hipStream_t st) {
 
 hipError_t launch_norm_quant(const NormQuantArgs& a, hipStream_t st) {
     const Shape sh = shape_of(a.r.K);
+    // A row per wave once every CU has rows enough for the constants in LDS to
+    // pay: measured at K = 5120, 1560 rows 13.6 us against 26.9, 384 rows 11.5
+    // against 14.8, 256 rows 11.6 against 8.9; at K = 4096, 1560 rows 12.1
+    // against 14.0, 768 rows 10.7 against 9.8.
     const int nw = (a.r.K + 511) / 512;
-    if (a.r.M >= 8 * (int64_t)device_cu_count() && nw <= 10) {
+    if (a.r.M > (nw > 8 ? 1 : 4) * (int64_t)device_cu_count() && nw <= 10) {
         const bool xf = a.r.x_dtype == MG_F32;
         switch (nw) {
 #define MG_WAVE(V) case V: return xf ? run_quant_wave<V, float>(a, st) : run_quant_wave<V, uint16_t>(a, st)
