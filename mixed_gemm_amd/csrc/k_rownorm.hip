@@ -1104,10 +1104,35 @@ int64_t resident(const void* kern, int threads, int lds) {
     return n;
 }
 
+// Workgroups of W waves of a row kernel that run on a CU at once.  A workgroup
+// starts only where every SIMD takes ceil(W / 4) more waves, and a SIMD takes
+// 6 waves of these kernels at most (their scalar registers): a grid that
+// leaves workgroups to a second round costs more than one with fewer.  Norm
+// of 11973 x 5120 bf16 (W = 5, 4 waves a SIMD): 46 us with 2 workgroups a CU,
+// 55 us with the 3 that 16 waves would hold.
+int64_t row_groups(const void* kern, int W) {
+    const int64_t per = resident(kern, 64, 0) / device_cu_count() / 4, waves = per < 6 ? (per > 1 ? per : 1) : 6;
+    const int64_t n = W % 4 ? (4 * waves - (W + 3) / 4 * 4) / W + 1 : 4 * waves / W;
+    return n > 1 ? n : 1;
+}
+
 template <int V, typename XT, typename YT>
 hipError_t run_rows(const RowArgs& a, int W, hipStream_t st) {
     const auto kern = row_kernel<V, XT, YT>;
-    const int64_t most = resident(reinterpret_cast<const void*>(kern), 64 * W, 0);
+    int64_t n = row_groups(reinterpret_cast<const void*>(kern), W);
+    // Memory is read fastest with about 18 KB of rows on their way to each CU:
+    // with 30000 rows of 2048, residual bf16 89 us with 2 workgroups a CU
+    // (16 KB), 97 us with 4; f32 150 us with 1 (16 KB), 168 us with 2 or 3.
+    // More workgroups pay for few rows (4099 rows, bf16: 18.1 us with 2, 17.0
+    // us with 4) and where a row waits longer, for a norm after the block or a
+    // partial vector (9973 rows of 2048 with it: 42 us with 2, 36 us with 4;
+    // 9973 rows of 2049: 57 us with 2, 47 us with 3).
+    if (a.M >= 32 * (int64_t)device_cu_count() && !a.has_post && a.K % 8 == 0) {
+        const int64_t row = a.K * (int64_t)(sizeof(XT) + (RowShape<V, XT, YT>::res ? sizeof(typename RowShape<V, XT, YT>::Y) : 0));
+        const int64_t best = (18 * 1024 + row / 2) / row;
+        if (n > best) n = best > 1 ? best : 1;
+    }
+    const int64_t most = n * device_cu_count();
     // consecutive rows where modulation rows may change often: a workgroup that
     // meets every group forms its coefficients once for each (the spread rows
     // read memory about 5 % faster)
