@@ -41,6 +41,7 @@ struct RowArgs {
     int32_t K;
     int32_t x_dtype, y_dtype, h_dtype;
     int32_t has_post, has_norm;
+    int32_t apart;        // O and H share no memory with X and Y (set by launch_rows)
     NormArgs post, norm;
     ModArgs gate, mod;
 };

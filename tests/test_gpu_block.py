@@ -266,6 +266,35 @@ def test_residual_in_place_and_plain_sum():
     assert torch.equal(O, (X.float() + Y.float()).bfloat16())
 
 
+@pytest.mark.parametrize("xt", ["bf16", "f32"])
+@pytest.mark.parametrize("M,K", [(5, 9), (700, 65), (1500, 2049), (1100, 2550), (900, 5121), (700, 8197), (520, 13823)])
+def test_partial_vectors_in_place(M, K, xt):
+    """Rows that end inside a vector: the same bytes in place, where the row's end is stored apart, as into other memory."""
+    rng = np.random.default_rng(K)
+    X, _ = rows(rng, M, K, xt)
+    Y, _ = rows(rng, M, K, xt)
+    sc, sh, g = modulation(rng, 2, K, "f32")
+    at = torch.arange(M, dtype=torch.int32, device="cuda") * 2 // M
+    at[M // 2] = -1
+    mod, gate = mg.Mod(scale=sc, shift=sh, index=at), mg.Mod(gate=g, index=at)
+    post = mg.Norm("rms", (1 + 0.2 * torch.randn(K, device="cuda")).bfloat16())
+    for p in (None, post):
+        O, H = torch.empty_like(X), torch.empty_like(Y)
+        mg.mg_residual_norm(X, Y, O, gate, p, mg.Norm(), mod, H)
+        x, y = X.clone(), Y.clone()
+        mg.mg_residual_norm(x, y, x, gate, p, mg.Norm(), mod, y)
+        assert torch.equal(x, O) and torch.equal(y, H)
+    x, y = X.clone(), Y.clone()
+    mg.mg_residual_norm(x, y, x, gate)
+    O = torch.empty_like(X)
+    mg.mg_residual_norm(X, Y, O, gate)
+    assert torch.equal(x, O)
+    H = torch.empty_like(X)
+    mg.mg_norm_mod(mg.Norm(), mod, X, H)
+    mg.mg_norm_mod(mg.Norm(), mod, x.copy_(X), x)
+    assert torch.equal(x, H)
+
+
 QUANT_CASES = [
     # M, K, k, x, kind, affine, modulation, its type, ld
     (1, 5120, 64, "bf16", "layer", None, "sample", "f32", 0),
