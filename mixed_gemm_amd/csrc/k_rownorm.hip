@@ -93,6 +93,7 @@ __device__ __forceinline__ void unpack(const RawAny& r, int32_t dtype, float (&v
 
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 // two floats rounded to bf16 (nearest even, NaN kept), the first in the low half
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     const f32x2 v = {lo, hi};
@@ -316,7 +317,7 @@ __device__ __forceinline__ void fold8(const RowThread<V, ODD>& t, const NormArgs
 template <int V, bool ODD>
 __device__ __forceinline__ void fold_all(const RowThread<V, ODD>& t, const NormArgs& n, const ModArgs& m, int row,
                                          float (&a)[V][8], float (&c)[V][8]) {
-    constexpr int G = V < 2 ? 1 : 2;
+    constexpr int G = V <= 2 ? 1 : 2;
 #pragma unroll
     for (int v = 0; v < V; v += G) {
         FoldRaw f[G];
@@ -389,25 +390,32 @@ struct RowSpan {
 template <int V, typename XT, typename YT>
 struct RowShape {
     static constexpr bool res = !std::is_void_v<YT>, ahead = V <= 4, keep = res ? V <= 2 : V <= 4;
+    static constexpr bool lds = res && V == 4;          // the folded coefficients in LDS, the gate in registers
+    static constexpr int lds_thread = lds ? V * 64 : 0; // bytes of a thread
     using Y = std::conditional_t<res, YT, uint16_t>;
     static constexpr int waves = V > 4 ? 4 : V == 4 ? 2 : V == 2 ? (res ? 2 : 4) : (res ? 4 : 5);    // per SIMD
 };
 
 // While a row is worked on, the next one's loads are in flight.  Up to 16384
-// channels (8192 with a residual) the folded coefficients, the gate and the
-// weights of the norm after the block stay in registers until the modulation
-// row changes; wider rows read them per row.  XT, YT: types of X and Y (YT
-// void: no residual step).
+// channels the folded coefficients and the gate are kept until the modulation
+// row changes, in registers, or the coefficients of more than 8192 channels
+// with a residual in LDS, each thread its own; wider rows read them per row,
+// as rows of more than 8192 do the weights of the norm after the block.  (Any
+// load of a row's body returns only after the next row's, so reading them per
+// row costs the time that the loads ahead are to hide.)  XT, YT: types of X
+// and Y (YT void: no residual step).
 template <int V, typename XT, typename YT>
 __global__ void __launch_bounds__(V <= 4 ? 512 : 1024) __attribute__((amdgpu_waves_per_eu(RowShape<V, XT, YT>::waves)))
 row_kernel(RowArgs a, RowSpan span) {
     using S = RowShape<V, XT, YT>;
-    constexpr bool RES = S::res, KEEP = S::keep;
+    constexpr bool RES = S::res, KEEP = S::keep, LDS = S::lds, GATE = RES && (KEEP || LDS);
     using Y = typename S::Y;
     __shared__ Pairs pairs;
+    extern __shared__ __attribute__((aligned(16))) uint8_t coefs[];      // a and c, 32 bytes each, per vector and thread
     int turn = 0;
     const RowThread<V> t(a.K);
-    float na[KEEP ? V : 1][8], nc[KEEP ? V : 1][8], ga[KEEP && RES ? V : 1][8], pw[KEEP && RES ? V : 1][8];
+    f32x4* const mine = reinterpret_cast<f32x4*>(coefs) + threadIdx.x;    // + T per 16 bytes: no bank conflicts, no barrier
+    float na[KEEP ? V : 1][8], nc[KEEP ? V : 1][8], ga[GATE ? V : 1][8], pw[KEEP && RES ? V : 1][8];
     int mi_of = -1, gi_of = -1;       // modulation rows that the kept coefficients belong to
     Raw8<XT> rx[V];
     Raw8<Y> ry[RES ? V : 1];
@@ -438,7 +446,7 @@ row_kernel(RowArgs a, RowSpan span) {
     load_row();
     while (true) {
         const int mi = __builtin_amdgcn_readfirstlane(mrow), gi = __builtin_amdgcn_readfirstlane(grow);
-        if constexpr (KEEP) {
+        if constexpr (KEEP || LDS) {
             const bool ng = RES && gi >= 0 && gi != gi_of;
             if (ng || (mi >= 0 && mi != mi_of)) {
                 RawAny rg[V];
@@ -451,15 +459,26 @@ row_kernel(RowArgs a, RowSpan span) {
                 }
                 if (mi >= 0 && mi != mi_of) {
                     const FoldArgs f = fold_args();
-                    fold_all(t, f.norm, f.mod, mi, na, nc);
+                    if constexpr (KEEP) fold_all(t, f.norm, f.mod, mi, na, nc);
+                    if constexpr (LDS) {
+#pragma unroll
+                        for (int v = 0; v < V; ++v) {
+                            fold8(t, f.norm, f.mod, mi, v, na[0], nc[0]);
+#pragma unroll
+                            for (int i = 0; i < 2; ++i) {
+                                mine[(4 * v + i) * t.T] = f32x4{na[0][4 * i], na[0][4 * i + 1], na[0][4 * i + 2], na[0][4 * i + 3]};
+                                mine[(4 * v + 2 + i) * t.T] = f32x4{nc[0][4 * i], nc[0][4 * i + 1], nc[0][4 * i + 2], nc[0][4 * i + 3]};
+                            }
+                        }
+                    }
                     mi_of = mi;
                 }
                 if (ng) {
 #pragma unroll
                     for (int v = 0; v < V; ++v) {
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) ga[RES ? v : 0][i] = 1.0f;
-                        if (gm.gate) unpack(rg[v], gm.dtype, ga[RES ? v : 0]);
+                        for (int i = 0; i < 8; ++i) ga[GATE ? v : 0][i] = 1.0f;
+                        if (gm.gate) unpack(rg[v], gm.dtype, ga[GATE ? v : 0]);
                     }
                 }
             }
@@ -493,12 +512,12 @@ row_kernel(RowArgs a, RowSpan span) {
                         }
                         post8(t, y[v], pw[KEEP ? v : 0], v, mean, rstd);
                     }
-                    if constexpr (!KEEP) {
+                    if constexpr (!GATE) {
                         const ModArgs m = mod_of(row_kernargs()->gate);
                         load_or_1(t, m.gate, gi * m.ld, m.dtype, v, ga[0]);
                     }
 #pragma unroll
-                    for (int i = 0; i < 8; ++i) x[v][i] = __builtin_fmaf(ga[KEEP ? v : 0][i], y[v][i], x[v][i]);
+                    for (int i = 0; i < 8; ++i) x[v][i] = __builtin_fmaf(ga[GATE ? v : 0][i], y[v][i], x[v][i]);
                     t.own(v, x[v]);
                 }
                 t.store8(a.O, oo, sizeof(XT) == 4 ? MG_F32 : MG_BF16, v, x[v], a.apart);
@@ -511,7 +530,13 @@ row_kernel(RowArgs a, RowSpan span) {
 #pragma unroll
             for (int v = 0; v < V; ++v) {
                 if (mi >= 0) {
-                    if constexpr (!KEEP) {
+                    if constexpr (LDS) {
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) {
+                            na[0][i] = mine[(4 * v + i / 4) * t.T][i % 4];
+                            nc[0][i] = mine[(4 * v + 2 + i / 4) * t.T][i % 4];
+                        }
+                    } else if constexpr (!KEEP) {
                         const FoldArgs f = fold_args();
                         fold8(t, f.norm, f.mod, mi, v, na[0], nc[0]);
                     }
@@ -1145,7 +1170,18 @@ hipError_t run_rows(const RowArgs& a, int W, hipStream_t st) {
     const int64_t group = a.mod.group < a.gate.group ? a.mod.group : a.gate.group;
     const bool same = !a.mod.index && !a.gate.index && (a.M + group - 1) / group * 8 <= chunk + 8;
     const int64_t blocks = same ? (a.M < most ? a.M : most) : (a.M + chunk - 1) / chunk;
-    hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(64 * W), 0, st, a, RowSpan{chunk, same ? blocks : 1});
+    constexpr int per = RowShape<V, XT, YT>::lds_thread;
+    if constexpr (per != 0) {
+        static thread_local int configured_dev = -1;
+        int dev = 0;
+        if (hipGetDevice(&dev) != hipSuccess) return hipErrorNoDevice;
+        if (configured_dev != dev) {
+            const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kern), hipFuncAttributeMaxDynamicSharedMemorySize, 512 * per);
+            if (e != hipSuccess) return e;
+            configured_dev = dev;
+        }
+    }
+    hipLaunchKernelGGL(kern, dim3((unsigned)blocks), dim3(64 * W), 64 * W * per, st, a, RowSpan{chunk, same ? blocks : 1});
     return hipGetLastError();
 }
 
