@@ -404,6 +404,17 @@ struct RowShape {
 // load of a row's body returns only after the next row's, so reading them per
 // row costs the time that the loads ahead are to hide.)  XT, YT: types of X
 // and Y (YT void: no residual step).
+//
+// Bound: memory, each row read and written once.  Norm with modulation of
+// 32760 x 5120, f32 in, bf16 out (1006 MB): 172-183 us, 5.5-5.8 TB/s (a 1 GiB
+// copy: 5.1); bf16 in 131 us, 5.1.  Gated residual with the next norm of
+// 75600 x 5120, f32 stream, bf16 block output (4.65 GB): 859 us, 5.4; bf16
+// stream 562 us, 5.5.  10000 x 13824 f32 316 us, 5.2.  9973 x 2049 bf16 with a
+// norm after the block and padding rows (164 MB) 51 us, 3.2: rows at odd
+// addresses and two exchanges a row.  One row: 3.8-4.0 us, the
+// launch and one trip to memory.  Reading a row twice (statistics, then the
+// result) would cost half as much again; two rows ahead instead of one
+// measured no gain, since the waves on a CU already fill its path to memory.
 template <int V, typename XT, typename YT>
 __global__ void __launch_bounds__(V <= 4 ? 512 : 1024) __attribute__((amdgpu_waves_per_eu(RowShape<V, XT, YT>::waves)))
 row_kernel(RowArgs a, RowSpan span) {
@@ -781,6 +792,12 @@ __device__ __forceinline__ void flush_unit(const NormQuantArgs& g, int64_t r0, i
 // of the operand's fragment blocks and scale windows).  Each row's codes are
 // staged in LDS and a unit's rows leave together.  Rows are row_kernel's, with
 // the same sums, so the codes are those of its bf16 output quantized.
+// Bound: for the few rows it runs, latency: the row, the statistics, the
+// coefficients' loads, the division and the blocks' maxima one after the other:
+// one row of 5120 7.7 us, 256 rows 8.9 us.  From more rows on the form below
+// is faster (32760 x 5120 f32: 352 us here); its 10 windows a row are the most
+// that registers hold, so wider rows stay here (8000 x 13824 bf16 112 us, 2.5
+// TB/s).
 template <int V, typename XT>
 __global__ void __launch_bounds__(V <= 4 ? 512 : 1024) __attribute__((amdgpu_waves_per_eu(V > 4 ? 4 : V == 4 ? 2 : V == 2 ? 3 : 4)))
 norm_quant_kernel(NormQuantArgs g, int R) {
@@ -883,6 +900,11 @@ norm_quant_kernel(NormQuantArgs g, int R) {
 // window with the next row.  V: windows of 512 channels, of which only the
 // last can be partial.  The sums are row_kernel's (those of its W waves), so
 // the bits are.
+// Bound: memory and the arithmetic of the quantize step together: 32760 x 5120
+// f32 (755 MB) 162-170 us, 4.4-4.7 TB/s; bf16 (420 MB, 83 us at a copy's rate)
+// 128 us, 3.3, where the arithmetic is the longer part.  A row per W waves with
+// the constants in registers took 352 us and 322 us, dividing the outlier
+// channels with the others 238 us and 198 us.
 template <int V>
 struct WaveShape {
     static constexpr int W = V <= 8 ? V : (V + 1) / 2;             // row_kernel's waves (and one or two vectors) for V windows
@@ -1099,7 +1121,9 @@ __global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) n
 }
 
 // Waves and vectors per thread for rows of K channels: 512 channels a wave and
-// vector, up to 8 waves, then more vectors, then more waves.
+// vector, up to 8 waves, then more vectors, then more waves.  At equal
+// bytes one vector was as fast as any from 512 to 4096 channels, and 5120 as
+// fast with 10 waves of one as with 5 of two (residual 38.7 and 38.9 us).
 struct Shape { int W, V; };
 Shape shape_of(int32_t K) {
     const int nw = (K + 511) / 512;
@@ -1164,7 +1188,8 @@ hipError_t run_rows(const RowArgs& a, int W, hipStream_t st) {
     }
     const int64_t most = n * device_cu_count();
     // consecutive rows where modulation rows may change often: a workgroup that
-    // meets every group forms its coefficients once for each (the spread rows
+    // meets every group forms its coefficients once for each (4099 x 1537 of 7
+    // samples: 12.6 us, spread 16.2; with one modulation row the spread rows
     // read memory about 5 % faster)
     const int64_t chunk = (a.M + most - 1) / most;
     const int64_t group = a.mod.group < a.gate.group ? a.mod.group : a.gate.group;
