@@ -291,28 +291,38 @@ hipError_t run_few(int tile, const FewArgs& a, hipStream_t st) {
 
 }  // namespace
 
-// The tile expected to be fastest.  A CU takes in about 90 bytes a nanosecond
-// of the operands from L2, whatever the tile, so a tile of tg x ng row groups
-// costs 16 K (tg + ng) bytes of that, plus what its workgroups spend outside
-// their K loop (own), as often as the workgroups go round the CUs, plus a
-// start (us).  The 256x256 tiles are bound by the matrix cores instead.
-// Measured (us, with gate and residual) against the 256x256 tiles: 5120 ->
-// 13824 at 1, 64, 256, 384 tokens 8.3, 10.7, 24.5, 32.0 (33.4, 33.8, 35.6,
-// 37.6; from about 500 tokens on they win), 13824 -> 5120 at 1, 64, 256, 1024
-// tokens 8.4, 12.7, 22.9, 67.9 (72.9, 73.5, 74.8, 77.0), 1568 -> 1056 at 777
-// tokens 6.6 (19.6).
-int few_tile(int64_t M, int32_t N, int32_t K) {
-    static const struct { int tg, ng; double start, own; } tiles[] = {
-        {1, 1, 3.2, 0.45}, {1, 2, 3.3, 0.9}, {2, 2, 6.2, 1.3}, {2, 3, 8.5, 1.5}};
+// The tile expected to be fastest, from a model of each one's time (us): a start,
+// and for every round of workgroups that the CUs make, the operands' way from
+// L2 (16 (tg + ng) bytes a channel; an outlier channel counts for 2 to 4, its
+// values take 4 times the bytes), what a workgroup spends outside its
+// K loop, and its output's and residual's way (`bytes` an element).  The
+// 256x256 tiles make their rounds one workgroup a CU; an incomplete round
+// leaves memory to the fewer outputs.  Fitted to 200 measured calls (M 24 to
+// 12000, K and N 256 to 13824, k 0 to 128, bias and GELU into bf16, gate and
+// residual in f32), whose choices lie 1.1 % above the best tile's time, 30 % at
+// worst; without k and the output's bytes 7.6 %, 150 % at worst (11496 tokens,
+// 416 -> 7552: 75 us with 256x256 tiles, 190 us with (2, 3)).  Measured against the 256x256 tiles, gate
+// and residual in bf16: 5120 -> 13824 at 1, 64, 256, 384 tokens 8.3, 10.7, 24.5,
+// 32.0 (33.4, 33.8, 35.6, 37.6), 13824 -> 5120 at 1, 64, 256, 1024 tokens 8.4,
+// 12.7, 22.9, 67.9 (72.9, 73.5, 74.8, 77.0), 1568 -> 1056 at 777 tokens 6.6
+// (19.6).
+int few_tile(int64_t M, int32_t N, int32_t K, int32_t k, int bytes) {
+    static const struct { int tg, ng; double start, own, chan, outlier, out, rest; } tiles[] = {
+        {1, 1, 3.3, 0.50, 2.00e-4, 2.4, 0.0167, 0.10},
+        {1, 2, 3.5, 0.51, 1.72e-4, 4.2, 0.0197, 0.65},
+        {2, 2, 3.2, 1.62, 1.87e-4, 3.9, 0.0197, 0.98},
+        {2, 3, 4.0, 2.72, 1.78e-4, 4.1, 0.0143, 0.91}};
     const double cus = device_cu_count();
     const double big = (double)((M + 255) / 256) * (double)((N + 255) / 256);
-    double best = 10.0 + __builtin_ceil(big / cus) * (K * 0.00446 + 16.0 * (big < cus ? big / cus : 1.0));
+    const double full = big < cus ? big / cus : 1.0;
+    double best = 9.3 + __builtin_ceil(big / cus) * (K * 0.00488 + k * 0.0212 + 0.97 + full * 3.49 * bytes);
     int tile = -1;
     for (int i = 0; i < 4; ++i) {
-        const int tg = tiles[i].tg, ng = tiles[i].ng;
-        const double wgs = (double)((M + 32 * tg - 1) / (32 * tg)) * (double)((N + 32 * ng - 1) / (32 * ng)), r = wgs / cus;
-        const double rounds = r <= 3.0 ? __builtin_ceil(r) : r + 0.3;
-        const double t = tiles[i].start + rounds * (16.0 * K * (tg + ng) / 90e3 + tiles[i].own);
+        const auto& f = tiles[i];
+        const double wgs = (double)((M + 32 * f.tg - 1) / (32 * f.tg)) * (double)((N + 32 * f.ng - 1) / (32 * f.ng));
+        // up to 3 workgroups share a CU and run their rounds together; then they stagger
+        const double r = wgs / cus, rounds = r <= 3.0 ? __builtin_ceil(r) : r + f.rest;
+        const double t = f.start + rounds * (f.chan * (K + f.outlier * k) * (f.tg + f.ng) + f.own + f.out * f.tg * f.ng * bytes);
         if (t < best) {
             best = t;
             tile = i;

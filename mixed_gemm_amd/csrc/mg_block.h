@@ -77,7 +77,7 @@ hipError_t launch_dual_gemm_ep(const uint8_t* Aq, const uint8_t* As, const uint1
 // The same for few rows, with K split over a workgroup's waves, and the tile
 // it would take (-1: the 256x256 tiles of launch_dual_gemm_ep are expected to
 // be faster).
-int few_tile(int64_t M, int32_t N, int32_t K);
+int few_tile(int64_t M, int32_t N, int32_t K, int32_t k, int bytes);
 hipError_t launch_dual_gemm_few(const uint8_t* Aq, const uint8_t* As, const uint16_t* XO, const uint8_t* Wq,
                                 const uint8_t* Ws, const uint16_t* WO, int64_t M, int32_t N, int32_t K, int32_t k,
                                 const EpArgs& e, void* Y, int32_t y_dtype, int tile, hipStream_t st);

@@ -148,7 +148,8 @@ int check_gemm_ep(const mg_plan* p, const mg_act* a, int64_t M, const mg_epilogu
 
 hipError_t run_gemm_ep(const mg_plan* p, const mg_act* a, int64_t M, const EpArgs& e, void* Y, int32_t y_dtype,
                        hipStream_t stream) {
-    const int tile = few_tile(M, p->d.N, p->d.K);
+    const int bytes = (y_dtype == MG_F32 ? 4 : 2) + (e.residual ? (e.residual_dtype == MG_F32 ? 4 : 2) : 0);
+    const int tile = few_tile(M, p->d.N, p->d.K, p->d.k, bytes);
     if (tile >= 0)
         return launch_dual_gemm_few(a->Aq, a->As, a->XO, p->Wq, p->Ws, p->WO, M, p->d.N, p->d.K, p->d.k, e, Y, y_dtype,
                                     tile, stream);

@@ -460,9 +460,20 @@ def test_gemm_epilogue(M, K, N, k, yt, bias, act, gate, res, mod, mt):
 @pytest.mark.parametrize("yt", ["bf16", "f32"])
 @pytest.mark.parametrize("res", [None, "bf16", "f32"])
 def test_every_form_of_the_large_tiles_epilogue(act, yt, res):
-    """Shapes that take the 256x256 tiles; each activation, output and residual
-    type, with one gate row, one per token, and none."""
-    M, K, N = 5000, 512, 2048
+    """A large output of few channels, most of it at memory's rate; each activation, output
+    and residual type, with one gate row, one per token, and none."""
+    _every_form(act, yt, res, 5000, 512, 2048)
+
+
+@pytest.mark.parametrize("act", ["none", "gelu", "silu"])
+@pytest.mark.parametrize("yt", ["bf16", "f32"])
+@pytest.mark.parametrize("res", [None, "bf16", "f32"])
+def test_every_form_of_the_256_wide_tiles_epilogue(act, yt, res):
+    """The same at a shape where every form takes the 256x256 tiles."""
+    _every_form(act, yt, res, 8190, 1312, 2048)
+
+
+def _every_form(act, yt, res, M, K, N):
     rng = np.random.default_rng(len(act) + 10 * len(yt))
     X, _ = rows(rng, M, K, "bf16")
     p = _quant_plan(rng, K, N, 7, X)
