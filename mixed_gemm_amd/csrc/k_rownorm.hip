@@ -266,7 +266,7 @@ __device__ __forceinline__ void row_stats(const float (&x)[V][8], const RowThrea
     const int l = (int)threadIdx.x & 15;
     const f32x2 p = l < t.W ? set[l] : f32x2{0.0f, 0.0f};
     mean = layer ? row16_sum(p[0]) * t.rK : 0.0f;
-    const float d = p[0] * t.rnl - mean;
+    const float d = __builtin_fmaf(p[0], t.rnl, -mean);
     const float Q = row16_sum(__builtin_fmaf(t.nl * d, d, p[1]));
     rstd = rsqrt_f32(__builtin_fmaf(Q, t.rK, eps));
 }
@@ -276,16 +276,14 @@ __device__ __forceinline__ void row_stats(const float (&x)[V][8], const RowThrea
 struct FoldRaw {
     RawAny scale, shift, weight, bias;
 };
-template <int V, bool ODD>
-__device__ __forceinline__ void fold_load(const RowThread<V, ODD>& t, const NormArgs& n, const ModArgs& m, int row, int v, FoldRaw& f) {
+template <typename T>
+__device__ __forceinline__ void fold_load(const T& t, const NormArgs& n, const ModArgs& m, int row, int v, FoldRaw& f) {
     load_any(m.scale, row * m.ld + t.at[v], m.dtype, f.scale);
     load_any(m.shift, row * m.ld + t.at[v], m.dtype, f.shift);
     load_any(n.bias, t.at[v], n.dtype, f.bias);
     load_any(n.weight, t.at[v], n.dtype, f.weight);
 }
-template <int V, bool ODD>
-__device__ __forceinline__ void fold_make(const RowThread<V, ODD>& t, const NormArgs& n, const ModArgs& m, const FoldRaw& f, int v,
-                                          float (&a)[8], float (&c)[8]) {
+__device__ __forceinline__ void fold_make(const NormArgs& n, const ModArgs& m, const FoldRaw& f, float (&a)[8], float (&c)[8]) {
     float w[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) { a[i] = 1.0f; c[i] = 0.0f; }
@@ -306,12 +304,12 @@ __device__ __forceinline__ void fold_make(const RowThread<V, ODD>& t, const Norm
         for (int i = 0; i < 8; ++i) a[i] *= w[i];
     }
 }
-template <int V, bool ODD>
-__device__ __forceinline__ void fold8(const RowThread<V, ODD>& t, const NormArgs& n, const ModArgs& m, int row, int v,
+template <typename T>
+__device__ __forceinline__ void fold8(const T& t, const NormArgs& n, const ModArgs& m, int row, int v,
                                       float (&a)[8], float (&c)[8]) {
     FoldRaw f;
     fold_load(t, n, m, row, v, f);
-    fold_make(t, n, m, f, v, a, c);
+    fold_make(n, m, f, a, c);
 }
 // of all vectors, two at a time
 template <int V, bool ODD>
@@ -324,7 +322,7 @@ __device__ __forceinline__ void fold_all(const RowThread<V, ODD>& t, const NormA
 #pragma unroll
         for (int k = 0; k < G; ++k) fold_load(t, n, m, row, v + k, f[k]);
 #pragma unroll
-        for (int k = 0; k < G; ++k) fold_make(t, n, m, f[k], v + k, a[v + k], c[v + k]);
+        for (int k = 0; k < G; ++k) fold_make(n, m, f[k], a[v + k], c[v + k]);
     }
 }
 // n a + c; the rounding of -mean rstd is as small as the mean's own
@@ -334,8 +332,8 @@ __device__ __forceinline__ void apply8(float (&x)[8], float mean, float rstd, co
     for (int i = 0; i < 8; ++i) x[i] = __builtin_fmaf(__builtin_fmaf(x[i], rstd, b), a[i], c[i]);
 }
 // 8 values of an optional array (1 without one)
-template <int V>
-__device__ __forceinline__ void load_or_1(const RowThread<V>& t, const void* p, int64_t row, int32_t dtype, int v, float (&g)[8]) {
+template <typename T>
+__device__ __forceinline__ void load_or_1(const T& t, const void* p, int64_t row, int32_t dtype, int v, float (&g)[8]) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) g[i] = 1.0f;
     if (p) t.load8(p, row, dtype, v, g);
@@ -367,8 +365,8 @@ __device__ __forceinline__ FoldArgs fold_args() {
 }
 
 // The norm after the block (weight pw; the rare bias is read where it is used).
-template <int V>
-__device__ __forceinline__ void post8(const RowThread<V>& t, float (&y)[8], const float (&pw)[8], int v, float mean, float rstd) {
+template <typename T>
+__device__ __forceinline__ void post8(const T& t, float (&y)[8], const float (&pw)[8], int v, float mean, float rstd) {
     const float b = -mean * rstd;
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[i] = __builtin_fmaf(y[i], rstd, b) * pw[i];
@@ -562,6 +560,121 @@ row_kernel(RowArgs a, RowSpan span) {
         }
         if (!more) break;
         if constexpr (!S::ahead) load_row();
+    }
+}
+
+// Rows of 8 to 128 channels, heads as a norm of queries and keys has them: 16
+// lanes take a row, a wave 4 (a wave each leaves most lanes idle: 75600 x 65,
+// residual bf16, 46 us against 12).  No barrier, one row ahead in flight.  The
+// sums are row_kernel's of one wave, so the bits are.  Bound: memory where rows
+// fill the lanes (75600 x 100, residual bf16, 12.2 us, 4.9 TB/s; norm of f32 into
+// bf16 8.9 us, 5.1), else the instructions of a row.
+struct NarrowThread {
+    int at[1];                      // channel of the lane's first element
+    __device__ __forceinline__ void load8(const void* p, int64_t row, int32_t dtype, int v, float (&x)[8]) const {
+        RawAny r;
+        load_any(p, row + at[v], dtype, r);
+        unpack(r, dtype, x);
+    }
+};
+template <typename XT, typename YT>
+__global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) row_narrow_kernel(RowArgs a) {
+    constexpr bool RES = !std::is_void_v<YT>;
+    using Y = std::conditional_t<RES, YT, uint16_t>;
+    const int K = a.K, col = 8 * ((int)threadIdx.x & 15);
+    NarrowThread t;
+    t.at[0] = col < K - 8 ? col : K - 8;
+    const int skip = col - t.at[0];                 // leading elements that are not the lane's own (8 and more: past the row)
+    const float nK = (float)K, rK = 1.0f / nK;
+    const bool norm = !RES || a.has_norm, post = RES && a.has_post;
+    const int64_t step = (int64_t)gridDim.x * 16;
+    int64_t r = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+    if (r >= a.M) return;
+    float na[8], nc[8], ga[8], pw[8];
+    int mi_of = -1, gi_of = -1, mrow = -1, grow = -1;
+    Raw8<XT> rx;
+    Raw8<Y> ry;
+    auto load_row = [&](int64_t row) {
+        load_raw(static_cast<const XT*>(a.X) + row * a.ldx + t.at[0], rx);
+        if constexpr (RES) load_raw(static_cast<const Y*>(a.Y) + row * a.ldy + t.at[0], ry);
+        if (norm) mrow = mod_row(a.mod, row);
+        if constexpr (RES) grow = mod_row(a.gate, row);
+    };
+    auto stats = [&](const float (&x)[8], int kind, float eps, float& mean, float& rstd) {
+        float s = 0.0f, q = 0.0f;
+        mean = 0.0f;
+        if (kind == MG_NORM_LAYER) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) s += i >= skip ? x[i] : 0.0f;
+            s = row16_sum(s);
+            mean = s * rK;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float d = i >= skip ? x[i] - mean : 0.0f;
+            q = __builtin_fmaf(d, d, q);
+        }
+        const float d = __builtin_fmaf(s, rK, -mean);
+        rstd = rsqrt_f32(__builtin_fmaf(__builtin_fmaf(nK * d, d, row16_sum(q)), rK, eps));
+    };
+    auto store8 = [&](void* p, int64_t row, bool f32, const float (&x)[8]) {
+        float* const pf = static_cast<float*>(p) + row + t.at[0];
+        uint16_t* const pb = static_cast<uint16_t*>(p) + row + t.at[0];
+        const u32x4 w = pack8_bf16(x);
+        if (skip < (a.apart ? 8 : 1)) {
+            if (f32) {
+                u32x4 u, v;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) { u[i] = __float_as_uint(x[i]); v[i] = __float_as_uint(x[4 + i]); }
+                reinterpret_cast<Piece16*>(pf)->v = u;
+                reinterpret_cast<Piece16*>(pf + 4)->v = v;
+            } else {
+                reinterpret_cast<Piece16*>(pb)->v = w;
+            }
+        } else if (skip < 8) {
+#pragma unroll
+            for (int i = 1; i < 8; ++i)
+                if (i >= skip) {
+                    if (f32) pf[i] = x[i];
+                    else pb[i] = (uint16_t)(w[i >> 1] >> (16 * (i & 1)));
+                }
+        }
+    };
+    if (post) load_or_1(t, a.post.weight, 0, a.post.dtype, 0, pw);
+    load_row(r);
+    for (; r < a.M; r += step) {
+        const int mi = mrow, gi = grow;
+        if (RES && gi >= 0 && gi != gi_of) {
+            load_or_1(t, a.gate.gate, gi * a.gate.ld, a.gate.dtype, 0, ga);
+            gi_of = gi;
+        }
+        if (mi >= 0 && mi != mi_of) {
+            fold8(t, a.norm, a.mod, mi, 0, na, nc);
+            mi_of = mi;
+        }
+        float x[8], y[8], mean, rstd;
+        unpack(rx, x);
+        if constexpr (RES) unpack(ry, y);
+        load_row(r + step < a.M ? r + step : r);
+        if constexpr (RES) {
+            if (post) stats(y, a.post.kind, a.post.eps, mean, rstd);
+            if (gi >= 0) {
+                if (post) post8(t, y, pw, 0, mean, rstd);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = __builtin_fmaf(ga[i], y[i], x[i]);
+            }
+            store8(a.O, r * a.ldo, sizeof(XT) == 4, x);
+        }
+        if (norm) {
+            stats(x, a.norm.kind, a.norm.eps, mean, rstd);
+            if (mi >= 0) {
+                apply8(x, mean, rstd, na, nc);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = 0.0f;
+            }
+            store8(a.H, r * a.ldh, a.h_dtype == MG_F32, x);
+        }
     }
 }
 
@@ -1064,7 +1177,7 @@ __global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) n
                 q = (lane & 15) == w ? qw[w] : q;
             }
             const float mean = layer ? row16_sum(s) * rK : 0.0f;
-            const float d = s * rnl - mean;
+            const float d = __builtin_fmaf(s, rnl, -mean);
             const float rstd = rsqrt_f32(__builtin_fmaf(row16_sum(__builtin_fmaf(nl * d, d, q)), rK, eps));
             uint8_t* const xo = g.XO + (r >> 5) * nso * kFragBlock + ((r & 31) << 4);
             const bool own = mi != loaded && mi >= 0;                 // another modulation row than the unit's
@@ -1210,6 +1323,14 @@ hipError_t run_rows(const RowArgs& a, int W, hipStream_t st) {
     return hipGetLastError();
 }
 
+template <typename XT, typename YT>
+hipError_t run_narrow(const RowArgs& a, hipStream_t st) {
+    const auto kern = row_narrow_kernel<XT, YT>;
+    const int64_t most = row_groups(reinterpret_cast<const void*>(kern), 4) * device_cu_count(), units = (a.M + 15) / 16;
+    hipLaunchKernelGGL(kern, dim3((unsigned)(units < most ? units : most)), dim3(256), 0, st, a);
+    return hipGetLastError();
+}
+
 template <int V, typename XT>
 hipError_t run_quant(const NormQuantArgs& a, int W, hipStream_t st) {
     const auto kern = norm_quant_kernel<V, XT>;
@@ -1270,10 +1391,15 @@ hipError_t launch_rows(const RowArgs& args, hipStream_t st) {
         hipLaunchKernelGGL(row_small_kernel, dim3((unsigned)((a.M + 255) / 256)), dim3(256), 0, st, a);
         return hipGetLastError();
     }
+    const bool xf = a.x_dtype == MG_F32, yf = a.y_dtype == MG_F32;
+    if (a.K <= 128) {
+        if (a.Y == nullptr) return xf ? run_narrow<float, void>(a, st) : run_narrow<uint16_t, void>(a, st);
+        if (xf) return yf ? run_narrow<float, float>(a, st) : run_narrow<float, uint16_t>(a, st);
+        return yf ? run_narrow<uint16_t, float>(a, st) : run_narrow<uint16_t, uint16_t>(a, st);
+    }
     const Shape sh = shape_of(a.K);
     return by_v(sh.V, [&](auto v) {
         constexpr int V = decltype(v)::value;
-        const bool xf = a.x_dtype == MG_F32, yf = a.y_dtype == MG_F32;
         if (a.Y == nullptr)
             return xf ? run_rows<V, float, void>(a, sh.W, st) : run_rows<V, uint16_t, void>(a, sh.W, st);
         if (xf) return yf ? run_rows<V, float, float>(a, sh.W, st) : run_rows<V, float, uint16_t>(a, sh.W, st);

@@ -89,6 +89,9 @@ NORM_CASES = [
     (3, 7, "bf16", "f32", "rms", "bf16", "token", "bf16", 0),
     (2, 8, "bf16", "bf16", "layer", "f32", "sample", "f32", 8),
     (300, 31, "f32", "bf16", "layer", None, "token", "f32", 1),
+    (2050, 128, "bf16", "bf16", "rms", "bf16", None, "f32", 0),
+    (1030, 121, "bf16", "f32", "layer", "f32", "token", "bf16", 7),
+    (70, 129, "f32", "f32", "layer", None, "token", "f32", 2),
     (64, 512, "bf16", "f32", "layer", "bf16", "sample", "bf16", 0),
     (7, 513, "bf16", "f32", "rms", None, "sample", "f32", 3),
     (33, 1537, "bf16", "bf16", "rms", "bf16", "token", "bf16", 9),
@@ -213,6 +216,9 @@ RES_CASES = [
     (5, 13824, "f32", "f32", "f32", True, "layer", "sample", "bf16", 8),
     (300, 77, "bf16", "f32", "f32", True, None, "token", "bf16", 1),
     (3, 30011, "f32", "bf16", "f32", False, "rms", "sample", "f32", 0),
+    (40, 8, "f32", "bf16", "f32", True, "layer", "token", "f32", 0),
+    (513, 64, "bf16", "f32", "bf16", True, "rms", "sample", "bf16", 0),
+    (600, 103, "f32", "f32", "bf16", False, "layer", "token", "f32", 5),
     (2, 65536, "bf16", "bf16", "f32", True, "layer", "sample", "f32", 0),
 ]
 
@@ -293,6 +299,31 @@ def test_partial_vectors_in_place(M, K, xt):
     mg.mg_norm_mod(mg.Norm(), mod, X, H)
     mg.mg_norm_mod(mg.Norm(), mod, x.copy_(X), x)
     assert torch.equal(x, H)
+
+
+@pytest.mark.parametrize("K", [8, 9, 63, 64, 100, 128, 129, 700])
+def test_rows_do_not_depend_on_their_number(K):
+    """A row's bits are the same in a call of many rows and of few."""
+    rng = np.random.default_rng(K)
+    M = 40003 if K <= 129 else 9001
+    X, _ = rows(rng, M, K, "bf16")
+    Y, _ = rows(rng, M, K, "f32")
+    sc, sh, g = modulation(rng, 3, K, "f32")
+    at = torch.arange(M, dtype=torch.int32, device="cuda") % 4 - 1
+    post = mg.Norm("layer", vec(rng, K, "bf16", 1.0), vec(rng, K, "bf16"))
+
+    def run(a, b):
+        i = at[a:b].contiguous()
+        mod, gate = mg.Mod(scale=sc, shift=sh, index=i), mg.Mod(gate=g, index=i)
+        o, h, n = torch.empty_like(X[a:b]), torch.empty_like(Y[a:b]), torch.empty_like(X[a:b])
+        mg.mg_residual_norm(X[a:b], Y[a:b], o, gate, post, mg.Norm("rms"), mod, h)
+        mg.mg_norm_mod(mg.Norm(), mod, X[a:b], n)
+        return o, h, n
+
+    whole = run(0, M)
+    for a, b in ((0, 1), (5, 22), (M - 331, M)):
+        for w, t in zip(whole, run(a, b)):
+            assert torch.equal(w[a:b], t)
 
 
 QUANT_CASES = [
