@@ -563,9 +563,10 @@ row_kernel(RowArgs a, RowSpan span) {
     }
 }
 
-// Rows of 8 to 128 channels, heads as a norm of queries and keys has them: 16
-// lanes take a row, a wave 4 (a wave each leaves most lanes idle: 75600 x 65,
-// residual bf16, 46 us against 12).  No barrier, one row ahead in flight.  The
+// Rows of 8 to 256 channels, heads as a norm of queries and keys has them: 16
+// or 32 lanes take a row, a wave 4 or 2 (a wave each leaves most lanes idle:
+// residual bf16 of 75600 rows, 65 wide 46 us against 12, 129 wide 47 us against
+// 20, 256 wide 46 us against 32).  No barrier, one row ahead in flight.  The
 // sums are row_kernel's of one wave, so the bits are.  Bound: memory where rows
 // fill the lanes (75600 x 100, residual bf16, 12.2 us, 4.9 TB/s; norm of f32 into
 // bf16 8.9 us, 5.1), else the instructions of a row.
@@ -577,18 +578,25 @@ struct NarrowThread {
         unpack(r, dtype, x);
     }
 };
-template <typename XT, typename YT>
+template <int LANES>
+__device__ __forceinline__ float lanes_sum(float v) {
+    v = row16_sum(v);
+    if constexpr (LANES == 32) v += __int_as_float(__builtin_amdgcn_ds_swizzle(__float_as_int(v), 0x401F));   // lane ^ 16
+    return v;
+}
+template <int LANES, typename XT, typename YT>
 __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) row_narrow_kernel(RowArgs a) {
+    constexpr int ROWS = 256 / LANES;               // of a workgroup
     constexpr bool RES = !std::is_void_v<YT>;
     using Y = std::conditional_t<RES, YT, uint16_t>;
-    const int K = a.K, col = 8 * ((int)threadIdx.x & 15);
+    const int K = a.K, col = 8 * ((int)threadIdx.x & (LANES - 1));
     NarrowThread t;
     t.at[0] = col < K - 8 ? col : K - 8;
     const int skip = col - t.at[0];                 // leading elements that are not the lane's own (8 and more: past the row)
     const float nK = (float)K, rK = 1.0f / nK;
     const bool norm = !RES || a.has_norm, post = RES && a.has_post;
-    const int64_t step = (int64_t)gridDim.x * 16;
-    int64_t r = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);
+    const int64_t step = (int64_t)gridDim.x * ROWS;
+    int64_t r = (int64_t)blockIdx.x * ROWS + threadIdx.x / LANES;
     if (r >= a.M) return;
     float na[8], nc[8], ga[8], pw[8];
     int mi_of = -1, gi_of = -1, mrow = -1, grow = -1;
@@ -606,7 +614,7 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) r
         if (kind == MG_NORM_LAYER) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) s += i >= skip ? x[i] : 0.0f;
-            s = row16_sum(s);
+            s = lanes_sum<LANES>(s);
             mean = s * rK;
         }
 #pragma unroll
@@ -615,7 +623,7 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) r
             q = __builtin_fmaf(d, d, q);
         }
         const float d = __builtin_fmaf(s, rK, -mean);
-        rstd = rsqrt_f32(__builtin_fmaf(__builtin_fmaf(nK * d, d, row16_sum(q)), rK, eps));
+        rstd = rsqrt_f32(__builtin_fmaf(__builtin_fmaf(nK * d, d, lanes_sum<LANES>(q)), rK, eps));
     };
     auto store8 = [&](void* p, int64_t row, bool f32, const float (&x)[8]) {
         float* const pf = static_cast<float*>(p) + row + t.at[0];
@@ -1258,7 +1266,7 @@ hipError_t by_v(int V, F&& f) {
 // device at once, looked up once per device, kernel and size.
 int64_t resident(const void* kern, int threads, int lds) {
     struct Entry { const void* k; int threads, lds, dev, n; };
-    static thread_local Entry cache[64] = {};
+    static thread_local Entry cache[96] = {};
     static thread_local int used = 0;
     int dev = 0;
     if (hipGetDevice(&dev) != hipSuccess) return device_cu_count();
@@ -1267,7 +1275,7 @@ int64_t resident(const void* kern, int threads, int lds) {
     int n = 0;
     if (hipOccupancyMaxActiveBlocksPerMultiprocessor(&n, kern, threads, lds) != hipSuccess || n < 1) n = 1;
     n *= device_cu_count();
-    if (used < 64) cache[used++] = Entry{kern, threads, lds, dev, n};
+    if (used < 96) cache[used++] = Entry{kern, threads, lds, dev, n};
     return n;
 }
 
@@ -1323,10 +1331,11 @@ hipError_t run_rows(const RowArgs& a, int W, hipStream_t st) {
     return hipGetLastError();
 }
 
-template <typename XT, typename YT>
+template <int LANES, typename XT, typename YT>
 hipError_t run_narrow(const RowArgs& a, hipStream_t st) {
-    const auto kern = row_narrow_kernel<XT, YT>;
-    const int64_t most = row_groups(reinterpret_cast<const void*>(kern), 4) * device_cu_count(), units = (a.M + 15) / 16;
+    const auto kern = row_narrow_kernel<LANES, XT, YT>;
+    constexpr int ROWS = 256 / LANES;
+    const int64_t most = row_groups(reinterpret_cast<const void*>(kern), 4) * device_cu_count(), units = (a.M + ROWS - 1) / ROWS;
     hipLaunchKernelGGL(kern, dim3((unsigned)(units < most ? units : most)), dim3(256), 0, st, a);
     return hipGetLastError();
 }
@@ -1392,10 +1401,14 @@ hipError_t launch_rows(const RowArgs& args, hipStream_t st) {
         return hipGetLastError();
     }
     const bool xf = a.x_dtype == MG_F32, yf = a.y_dtype == MG_F32;
-    if (a.K <= 128) {
-        if (a.Y == nullptr) return xf ? run_narrow<float, void>(a, st) : run_narrow<uint16_t, void>(a, st);
-        if (xf) return yf ? run_narrow<float, float>(a, st) : run_narrow<float, uint16_t>(a, st);
-        return yf ? run_narrow<uint16_t, float>(a, st) : run_narrow<uint16_t, uint16_t>(a, st);
+    if (a.K <= 256) {
+        auto run = [&](auto lanes) {
+            constexpr int L = decltype(lanes)::value;
+            if (a.Y == nullptr) return xf ? run_narrow<L, float, void>(a, st) : run_narrow<L, uint16_t, void>(a, st);
+            if (xf) return yf ? run_narrow<L, float, float>(a, st) : run_narrow<L, float, uint16_t>(a, st);
+            return yf ? run_narrow<L, uint16_t, float>(a, st) : run_narrow<L, uint16_t, uint16_t>(a, st);
+        };
+        return a.K <= 128 ? run(std::integral_constant<int, 16>{}) : run(std::integral_constant<int, 32>{});
     }
     const Shape sh = shape_of(a.K);
     return by_v(sh.V, [&](auto v) {

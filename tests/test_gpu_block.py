@@ -92,6 +92,8 @@ NORM_CASES = [
     (2050, 128, "bf16", "bf16", "rms", "bf16", None, "f32", 0),
     (1030, 121, "bf16", "f32", "layer", "f32", "token", "bf16", 7),
     (70, 129, "f32", "f32", "layer", None, "token", "f32", 2),
+    (515, 256, "bf16", "bf16", "layer", "bf16", "sample", "f32", 0),
+    (70, 257, "f32", "f32", "layer", None, "token", "f32", 2),
     (64, 512, "bf16", "f32", "layer", "bf16", "sample", "bf16", 0),
     (7, 513, "bf16", "f32", "rms", None, "sample", "f32", 3),
     (33, 1537, "bf16", "bf16", "rms", "bf16", "token", "bf16", 9),
@@ -219,6 +221,7 @@ RES_CASES = [
     (40, 8, "f32", "bf16", "f32", True, "layer", "token", "f32", 0),
     (513, 64, "bf16", "f32", "bf16", True, "rms", "sample", "bf16", 0),
     (600, 103, "f32", "f32", "bf16", False, "layer", "token", "f32", 5),
+    (300, 251, "bf16", "bf16", "f32", True, "layer", "token", "f32", 3),
     (2, 65536, "bf16", "bf16", "f32", True, "layer", "sample", "f32", 0),
 ]
 
@@ -273,7 +276,7 @@ def test_residual_in_place_and_plain_sum():
 
 
 @pytest.mark.parametrize("xt", ["bf16", "f32"])
-@pytest.mark.parametrize("M,K", [(5, 9), (700, 65), (1500, 2049), (1100, 2550), (900, 5121), (700, 8197), (520, 13823)])
+@pytest.mark.parametrize("M,K", [(5, 9), (700, 65), (700, 203), (1500, 2049), (1100, 2550), (900, 5121), (700, 8197), (520, 13823)])
 def test_partial_vectors_in_place(M, K, xt):
     """Rows that end inside a vector: the same bytes in place, where the row's end is stored apart, as into other memory."""
     rng = np.random.default_rng(K)
@@ -301,11 +304,11 @@ def test_partial_vectors_in_place(M, K, xt):
     assert torch.equal(x, H)
 
 
-@pytest.mark.parametrize("K", [8, 9, 63, 64, 100, 128, 129, 700])
+@pytest.mark.parametrize("K", [8, 9, 63, 64, 100, 128, 129, 192, 256, 257, 700])
 def test_rows_do_not_depend_on_their_number(K):
     """A row's bits are the same in a call of many rows and of few."""
     rng = np.random.default_rng(K)
-    M = 40003 if K <= 129 else 9001
+    M = 40003 if K <= 257 else 9001
     X, _ = rows(rng, M, K, "bf16")
     Y, _ = rows(rng, M, K, "f32")
     sc, sh, g = modulation(rng, 3, K, "f32")
