@@ -1102,6 +1102,9 @@ __global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) n
     float xo0 = outlier_x(row_at(r0 + wave), ol);
     auto mod_rows = [&](int64_t r) { return lane < 8 && r + lane < M ? mod_row(a.mod, r + lane) : -1; };
     int mis = mod_rows(r0);
+    // every wave reads what all of them have put into LDS above; a first unit of
+    // padding rows meets no barrier of the modulation's below
+    __syncthreads();
     for (; r0 < Mp; r0 += step) {
         const int64_t r = r0 + wave;
         const int live = r0 >= M ? 0 : M - r0 < 8 ? (int)(M - r0) : 8;

@@ -384,6 +384,38 @@ def test_norm_quantize_is_norm_then_quantize(M, K, k, xt, kind, affine, mod, mt,
         assert np.array_equal(x, y), f"{n}: {int((x != y).sum())} of {x.size} bytes differ"
 
 
+@pytest.mark.parametrize("M,K,k,xt", [(2500, 5120, 64, "f32"), (700, 4640, 33, "bf16"), (4099, 2048, 17, "bf16"),
+                                      (1100, 32, 3, "f32")])
+@pytest.mark.parametrize("where", ["first", "last", "all"])
+def test_norm_quantize_of_long_runs_of_padding(M, K, k, xt, where):
+    """Workgroups whose first rows are all padding: the bytes of the two steps.  A call with infinite
+    scales goes ahead, so that constants left in LDS by it would show as codes other than 0."""
+    rng = np.random.default_rng(M + K)
+    X, _ = rows(rng, M, K, xt)
+    sc, sh, _ = modulation(rng, 3, K, "f32")
+    idx = rng.integers(0, 3, M).astype(np.int32)
+    run = {"first": slice(0, M - M // 8), "last": slice(M // 8, M), "all": slice(0, M)}[where]
+    idx[run] = np.where(rng.random(len(idx[run])) < 0.5, -1, 3)
+    norm, m = mg.Norm(), mg.Mod(scale=sc, shift=sh, index=torch.from_numpy(idx).cuda())
+    H = torch.empty(M, K, dtype=torch.bfloat16, device="cuda")
+    mg.mg_norm_mod(norm, m, X, H)
+    p = _quant_plan(rng, K, 32, k, X.bfloat16())
+    a, f = mg.Act.empty(p.desc, M), mg.Act.empty(p.desc, M)
+    left = mg.Plan.from_state(p.state())
+    left.s = torch.full_like(p.s, float("inf"))
+    left.rcp = torch.full_like(p.rcp, float("inf"))
+    mg.mg_norm_quantize_act(left, norm, mg.Mod(scale=sc[:1], shift=sh[:1]), X, f)
+    for t in (f.Aq, f.As, f.XO):
+        t.fill_(0xA5)
+    mg.mg_quantize_act(p, H, a)
+    mg.mg_norm_quantize_act(p, norm, m, X, f)
+    torch.cuda.synchronize()
+    for n in ("Aq", "As", "XO"):
+        assert torch.equal(getattr(a, n), getattr(f, n)), n
+    if where == "all":
+        assert not any(t.any() for t in (f.Aq, f.As, f.XO))
+
+
 @pytest.mark.parametrize("M", [40, 2100])
 def test_norm_quantize_with_scales_out_of_the_fast_range(M):
     """Smoothing scales far from 1 and rows of tiny values: the exact division's codes."""
