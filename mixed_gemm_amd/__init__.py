@@ -552,8 +552,9 @@ def _act_struct(desc, act: "Act", M: int | None = None) -> mg_act:
     if (m != M and M is not None) or Aq.dtype != torch.uint8 or Aq.shape != (g, ns, 1024) \
             or _nbytes(As) != -(-m // 256) * -(-desc.K // 512) * 4096 or _nbytes(XO) != g * nso * 1024:
         _check_act(desc, act, M)
-    if not (Aq.is_cuda and Aq.is_contiguous() and As.is_contiguous() and XO.is_contiguous()):
-        return act.c()                                                 # raises
+    for t in (Aq, As, XO):
+        if not (t.is_cuda and t.is_contiguous()):
+            _ptr(t)                                                    # raises, unless it is empty
     return mg_act(Aq.data_ptr() or None, As.data_ptr() or None, XO.data_ptr() or None)
 
 
