@@ -959,6 +959,7 @@ def ffn_sublayer_stats(calib_batches, W0: torch.Tensor, norm: Norm, bias0: torch
     """Calibration statistics of a sublayer's two projections, from (x, mod)
     batches of its input rows and their modulation: ffn.0's from h = norm(x)
     (1 + scale) + shift, ffn.2's from the unquantized gelu(h W0^T + bias0).
+    Padding tokens count in neither (their h and their hidden row are 0 here).
     Returns (act_max0, act_max2) for ffn_block_plans."""
     N0, K0 = W0.shape
     act0 = torch.empty(K0, dtype=torch.float32, device=W0.device)
@@ -966,8 +967,9 @@ def ffn_sublayer_stats(calib_batches, W0: torch.Tensor, norm: Norm, bias0: torch
     mg_calib_reset(act0, stream)
     mg_calib_reset(act2, stream)
     ref0 = reference_plan(W0, stream)
-    ep = Epilogue(bias0, "gelu")
     for x, mod in calib_batches:
+        index = None if mod is None else mod.tensors[3]
+        ep = Epilogue(bias0, "gelu", None if index is None else Mod(index=index, rows=mod.c.rows))
         h = torch.empty((x.shape[0], K0), dtype=torch.bfloat16, device=x.device)
         mg_norm_mod(norm, mod, x, h, stream)
         mg_calib_act(h, act0, stream)

@@ -723,6 +723,35 @@ def test_ffn_sublayer_quantized():
     assert ((out - ref).norm() / (ref - xs[0]).norm()).item() < 0.5     # 4 bits: a coarse check of the wiring
 
 
+@pytest.mark.parametrize("M", [90, 2300])
+def test_sublayer_statistics_leave_padding_out(M):
+    """ffn.2's maxima are those of gelu(h W0^T + bias0) over the live tokens, where the hidden row of
+    a padding token, gelu(bias0), would exceed them.  h's rounding to bf16 (2^-8 of its value, counted
+    twice for the f32 error below it) passes through W0, the hidden value is rounded to bf16 once more."""
+    rng = np.random.default_rng(M)
+    K, N = 256, 512
+    # W0 < 0 and h > 0 in the mean: every live token's hidden row lies below the bias alone
+    W0 = torch.from_numpy(-np.abs(rng.standard_normal((N, K))) * 0.01).cuda().bfloat16()
+    b0 = torch.from_numpy(8.0 + rng.random(N)).float().cuda()
+    sc, sh, _ = modulation(rng, 2, K, "f32")
+    sh.abs_().add_(2.0)
+    x, _ = rows(rng, M, K, "f32")
+    idx = rng.integers(-1, 3, M).astype(np.int32)
+    i = block.rows_of(M, 2, idx)
+    m = mg.Mod(scale=sc, shift=sh, index=torch.from_numpy(idx).cuda())
+    act0, act2 = mg.ffn_sublayer_stats([(x, m)], W0, mg.Norm(), b0)
+    h = block.modulate(block.norm(f64(x)), i, f64(sc), f64(sh))[i >= 0]
+    v = h @ f64(W0).T + f64(b0)
+    g = np.abs(block.activation(v, "gelu"))
+    r = 2.0 ** -8
+    dg = 1.13 * (2 * r * np.abs(h)) @ np.abs(f64(W0)).T + 1e-4
+    top = g.max(axis=0)
+    bound = dg.max(axis=0) * (1 + r) + r * top
+    assert_close(f64(act2), top, bound, "f32", "act2")
+    assert (block.activation(f64(b0), "gelu") > top + 2 * bound).all(), "the case would not show the padding"
+    assert np.abs(f64(act0) - np.abs(h).max(axis=0)).max() <= 2 * r * np.abs(h).max()
+
+
 # ------------------------------------------------------------------ refusals
 
 def test_binding_refuses_what_does_not_fit():
