@@ -208,6 +208,15 @@ __device__ __forceinline__ float rsqrt_f32(float v) {
     return tiny ? r * 0x1p50f : r;
 }
 
+// sum / K: the product with RN(1 / K) corrected by its remainder (P. Markstein,
+// 1990), the quotient correctly rounded.  The product alone is up to 1.5 units
+// of the mean off, which 1 / sqrt(eps) = 1000 made 0.03 of a constant row of 100.
+__device__ __forceinline__ float mean_of(float sum, int K, float rK) {
+    asm volatile("" : "+s"(K));      // converted here, not held in a vector register across the rows
+    const float m = sum * rK;
+    return __builtin_fmaf(__builtin_fmaf(-m, (float)K, sum), rK, m);
+}
+
 // mean (0 for rms) and 1 / sqrt(var + eps) of the row x: the parallel variance
 // formula over the waves, whose pairs the 16 lanes of a row take one each.
 template <int V, bool ODD>
@@ -265,7 +274,7 @@ __device__ __forceinline__ void row_stats(const float (&x)[V][8], const RowThrea
     __syncthreads();
     const int l = (int)threadIdx.x & 15;
     const f32x2 p = l < t.W ? set[l] : f32x2{0.0f, 0.0f};
-    mean = layer ? row16_sum(p[0]) * t.rK : 0.0f;
+    mean = layer ? mean_of(row16_sum(p[0]), t.K, t.rK) : 0.0f;
     const float d = __builtin_fmaf(p[0], t.rnl, -mean);
     const float Q = row16_sum(__builtin_fmaf(t.nl * d, d, p[1]));
     rstd = rsqrt_f32(__builtin_fmaf(Q, t.rK, eps));
@@ -325,11 +334,14 @@ __device__ __forceinline__ void fold_all(const RowThread<V, ODD>& t, const NormA
         for (int k = 0; k < G; ++k) fold_make(n, m, f[k], a[v + k], c[v + k]);
     }
 }
-// n a + c; the rounding of -mean rstd is as small as the mean's own
+// n of one channel.  x - mean is formed first, exact where x is near the mean:
+// as x rstd - mean rstd it would carry the rounding of a product that the
+// distance to the mean can be any small part of.
+__device__ __forceinline__ float normed(float x, float mean, float rstd) { return (x - mean) * rstd; }
+// n a + c
 __device__ __forceinline__ void apply8(float (&x)[8], float mean, float rstd, const float (&a)[8], const float (&c)[8]) {
-    const float b = -mean * rstd;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = __builtin_fmaf(__builtin_fmaf(x[i], rstd, b), a[i], c[i]);
+    for (int i = 0; i < 8; ++i) x[i] = __builtin_fmaf(normed(x[i], mean, rstd), a[i], c[i]);
 }
 // 8 values of an optional array (1 without one)
 template <typename T>
@@ -367,9 +379,8 @@ __device__ __forceinline__ FoldArgs fold_args() {
 // The norm after the block (weight pw; the rare bias is read where it is used).
 template <typename T>
 __device__ __forceinline__ void post8(const T& t, float (&y)[8], const float (&pw)[8], int v, float mean, float rstd) {
-    const float b = -mean * rstd;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = __builtin_fmaf(y[i], rstd, b) * pw[i];
+    for (int i = 0; i < 8; ++i) y[i] = normed(y[i], mean, rstd) * pw[i];
     const RowKernargs p = row_kernargs();
     if (p->post.bias) {
         float c[8];
@@ -615,7 +626,7 @@ __global__ void __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) r
 #pragma unroll
             for (int i = 0; i < 8; ++i) s += i >= skip ? x[i] : 0.0f;
             s = lanes_sum<LANES>(s);
-            mean = s * rK;
+            mean = mean_of(s, K, rK);
         }
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -698,8 +709,8 @@ __global__ void __launch_bounds__(256) row_small_kernel(RowArgs a) {
         for (int j = 0; j < K; ++j) q = __builtin_fmaf(x[j] - mean, x[j] - mean, q);
         rstd = rsqrt_f32(q / (float)K + n.eps);
     };
-    auto normed = [&](float x, int j, const NormArgs& n, float mean, float rstd) {
-        x = (x - mean) * rstd;
+    auto norm1 = [&](float x, int j, const NormArgs& n, float mean, float rstd) {
+        x = normed(x, mean, rstd);
         if (n.weight) x *= load_elem(n.weight, j, n.dtype);
         return n.bias ? x + load_elem(n.bias, j, n.dtype) : x;
     };
@@ -715,7 +726,7 @@ __global__ void __launch_bounds__(256) row_small_kernel(RowArgs a) {
         if (a.has_post) stats(y, a.post, mean, rstd);
         for (int j = 0; j < K; ++j) {
             if (gi >= 0) {
-                const float b = a.has_post ? normed(y[j], j, a.post, mean, rstd) : y[j];
+                const float b = a.has_post ? norm1(y[j], j, a.post, mean, rstd) : y[j];
                 x[j] = __builtin_fmaf(a.gate.gate ? load_elem(a.gate.gate, gi * a.gate.ld + j, a.gate.dtype) : 1.0f, b, x[j]);
             }
             put(a.O, r * a.ldo + j, a.x_dtype, x[j]);
@@ -727,7 +738,7 @@ __global__ void __launch_bounds__(256) row_small_kernel(RowArgs a) {
         for (int j = 0; j < K; ++j) {
             float h = 0.0f;
             if (mi >= 0) {
-                h = normed(x[j], j, a.norm, mean, rstd);
+                h = norm1(x[j], j, a.norm, mean, rstd);
                 if (a.mod.scale) h *= 1.0f + load_elem(a.mod.scale, mi * a.mod.ld + j, a.mod.dtype);
                 if (a.mod.shift) h += load_elem(a.mod.shift, mi * a.mod.ld + j, a.mod.dtype);
             }
@@ -863,7 +874,7 @@ __device__ __forceinline__ void outlier_fold(OutlierLane& o, const FoldArgs& f, 
 }
 __device__ __forceinline__ void outlier_put(const OutlierLane& o, float x, float mean, float rstd, bool pad, uint8_t* xo) {
     if (o.at < 0) return;
-    const float h = __builtin_fmaf(__builtin_fmaf(x, rstd, -mean * rstd), o.a, o.c);
+    const float h = __builtin_fmaf(normed(x, mean, rstd), o.a, o.c);
     const float q = __fdiv_rn(bf16_to_f32(pack_bf16(h, 0.0f) & 0xFFFFu), o.s);
     *reinterpret_cast<uint16_t*>(xo + o.at) = o.j < 0 || pad ? 0 : (uint16_t)f32_to_bf16_rne(q);
 }
@@ -1187,7 +1198,7 @@ __global__ void __launch_bounds__(512) __attribute__((amdgpu_waves_per_eu(2))) n
                 s = (lane & 15) == w ? sw[w] : s;
                 q = (lane & 15) == w ? qw[w] : q;
             }
-            const float mean = layer ? row16_sum(s) * rK : 0.0f;
+            const float mean = layer ? mean_of(row16_sum(s), K, rK) : 0.0f;
             const float d = __builtin_fmaf(s, rnl, -mean);
             const float rstd = rsqrt_f32(__builtin_fmaf(row16_sum(__builtin_fmaf(nl * d, d, q)), rK, eps));
             uint8_t* const xo = g.XO + (r >> 5) * nso * kFragBlock + ((r & 31) << 4);

@@ -170,6 +170,42 @@ def test_norm_of_rows_far_from_zero(K):
     assert norm_bound(x, n, 1.0, 0.0, K, "layer", 1e-6).max() < 0.05
 
 
+@pytest.mark.parametrize("xt", ["bf16", "f32"])
+@pytest.mark.parametrize("K", [8, 100, 129, 255, 257, 513, 1536, 2049, 5120, 8200, 13824, 20000])
+def test_constant_rows_are_centred_exactly(K, xt):
+    """The sum of up to 2^16 equal values of 8 bits is exact in f32, and the mean is their quotient
+    correctly rounded: the value itself.  So the norm is 0, and its output the shift."""
+    v = torch.tensor([1.0, 3.0, -100.0, 240.0, 0.0625 * 37, -251.0], device="cuda")
+    X = v[:, None].expand(-1, K).contiguous().to(TYPES[xt])
+    H, O, Y = torch.empty(6, K, device="cuda"), torch.empty_like(X), torch.zeros_like(X)
+    mg.mg_norm_mod(mg.Norm("layer"), None, X, H)
+    assert (H == 0).all(), H.abs().amax(1)
+    H.fill_(7.0)
+    mg.mg_residual_norm(X, Y, O, None, None, mg.Norm("layer"), None, H)
+    assert torch.equal(O, X) and (H == 0).all()
+    mg.mg_residual_norm(Y, X, O, None, mg.Norm("layer"))
+    assert (O == 0).all()
+    sh = vec(np.random.default_rng(K), K, "f32")[None]
+    mg.mg_norm_mod(mg.Norm("layer"), mg.Mod(scale=sh, shift=sh), X, H)
+    assert torch.equal(H, sh.expand(6, K))
+
+
+@pytest.mark.parametrize("K", [96, 250, 1536, 5120, 5121, 13824])
+def test_rows_on_a_grid_far_from_zero(K):
+    """bf16 values 99.5, 100, 100.5: the sum is exact, so the mean is off by its rounding alone (u of
+    it), and x - mean is exact or off by u of itself."""
+    rng = np.random.default_rng(K)
+    X = torch.from_numpy(100.0 + 0.5 * rng.integers(-1, 2, (40, K))).cuda().bfloat16()
+    H = torch.empty(40, K, device="cuda")
+    mg.mg_norm_mod(mg.Norm(), None, X, H)
+    x = f64(X)
+    n, mean = block.norm(x), x.mean(axis=1, keepdims=True)
+    rstd = 1 / np.sqrt(x.var(axis=1, keepdims=True) + 1e-6)
+    # the variance: (D + 6) u relative, and the square of the means' errors
+    bound = rstd * U * np.abs(mean) + np.abs(n) * (U * (_depth(K) / 2 + 12) + (4 * U * 100 * rstd) ** 2)
+    assert_close(f64(H), n, bound, "f32", "H")
+
+
 def test_constant_zero_and_extreme_rows():
     K = 200
     X = torch.zeros(5, K, device="cuda")
