@@ -332,8 +332,12 @@ int mg_dual_gemm_gelu_quant(const mg_plan* p0, const mg_act* a0, int64_t M, cons
  * is rounded once, to nearest even, to the type it is stored in.  In these
  * calls X, Y, O, H are rows `ld` elements apart (ld >= their width) that only
  * need their element's alignment; finite inputs are not required: NaN and
- * infinities spread as the formulas say, except that padding rows take
- * nothing from their inputs (below). ---- */
+ * infinities spread as the formulas say, within their row, except that padding
+ * rows take nothing from their inputs (below).  Two limits: a norm's bias is
+ * multiplied by 1 + scale before it is added, so where that product is
+ * infinite the sum of two infinities can be NaN; and a norm that is not finite
+ * has unspecified codes in mg_norm_quantize_act, as everywhere in the quantize
+ * step. ---- */
 
 typedef enum { MG_NORM_LAYER = 0, MG_NORM_RMS = 1 } mg_norm_kind;
 
@@ -398,7 +402,8 @@ int mg_residual_norm(const mg_residual* a, int64_t M, int32_t K, hipStream_t str
 
 /* mg_norm_mod into bf16 and mg_quantize_act of the result in one pass: the
  * operands of the projection behind the norm, bit for bit what those two
- * calls write (pads included), without writing the normalized rows.
+ * calls write (pads included) in every row whose norm is finite, without
+ * writing the normalized rows.
  * K = p->d.K. */
 int mg_norm_quantize_act(const mg_plan* p, const mg_norm* norm, const mg_mod* mod, const void* X, int32_t dtype,
                          int64_t ldx, int64_t M, const mg_act* a, hipStream_t stream);

@@ -713,7 +713,7 @@ def mg_residual_norm(X: torch.Tensor, Y: torch.Tensor, O: torch.Tensor, gate: Mo
 
 
 def mg_norm_quantize_act(plan: Plan, norm: Norm, mod: Mod | None, X: torch.Tensor, act: Act, stream=None) -> None:
-    """mg_norm_mod into bf16, then mg_quantize_act, in one pass (the same bits)."""
+    """mg_norm_mod into bf16, then mg_quantize_act, in one pass (the same bits in rows whose norm is finite)."""
     desc = plan.desc
     M, ldx = _rows(X, "X", desc.K)
     a = _act_struct(desc, act, M)

@@ -281,7 +281,8 @@ __device__ __forceinline__ void row_stats(const float (&x)[V][8], const RowThrea
 }
 
 // A norm with its modulation folded to n a + c, n = (x - mean) rstd: a = w (1 +
-// scale_i), c = b (1 + scale_i) + shift_i of 8 channels.
+// scale_i), c = b (1 + scale_i) + shift_i of 8 channels (an infinite 1 + scale
+// meets a bias as inf - inf where n w + b, formed first, would have kept a sign).
 struct FoldRaw {
     RawAny scale, shift, weight, bias;
 };

@@ -420,6 +420,38 @@ def test_norm_quantize_is_norm_then_quantize(M, K, k, xt, kind, affine, mod, mt,
         assert np.array_equal(x, y), f"{n}: {int((x != y).sum())} of {x.size} bytes differ"
 
 
+@pytest.mark.parametrize("M,K", [(40, 1024), (2100, 1024), (300, 5120), (40, 13824)])
+@pytest.mark.parametrize("kind", ["layer", "rms"])
+def test_norm_quantize_keeps_nan_and_infinity_in_their_rows(M, K, kind):
+    """Rows whose norm is not finite have unspecified codes, as in mg_quantize_act; all others have the
+    bytes of the two steps, padding rows 0 whatever their input holds."""
+    from tests.gpu_util import aq_rows, outlier_cols, scale_rows
+    rng = np.random.default_rng(K + M)
+    X, _ = rows(rng, M, K, "f32")
+    k = 40
+    p = _quant_plan(rng, K, 32, k, X.bfloat16())
+    X[3, K // 2] = float("nan")
+    X[5, 7] = float("inf")
+    X[6, K - 1] = -float("inf")
+    X[M - 2, 11], X[M - 2, 12] = -float("nan"), float("inf")
+    sc, sh, _ = modulation(rng, 4, K, "f32")
+    sh[1, 5], sh[1, K - 9] = float("inf"), -float("inf")
+    sh[2, p.O[0]], sh[2, 70] = float("nan"), -float("nan")
+    at = torch.arange(M, dtype=torch.int32, device="cuda") % 5
+    X[at == 4] = float("nan")                                             # padding
+    norm, m = mg.Norm(kind), mg.Mod(scale=sc, shift=sh, index=at)
+    H = torch.empty(M, K, dtype=torch.bfloat16, device="cuda")
+    mg.mg_norm_mod(norm, m, X, H)
+    fine = host(torch.isfinite(H).all(1))
+    assert 0 < fine.sum() < M and fine[host(at) == 4].all()
+    a, f = mg.Act.empty(p.desc, M), mg.Act.empty(p.desc, M)
+    mg.mg_quantize_act(p, H, a)
+    mg.mg_norm_quantize_act(p, norm, m, X, f)
+    for x, y in zip(*[(aq_rows(z.Aq, M, K), scale_rows(z.As, M, K), outlier_cols(z.XO, M, k)) for z in (a, f)]):
+        assert np.array_equal(x[fine], y[fine])
+        assert not y[host(at) == 4].any()
+
+
 @pytest.mark.parametrize("M,K,k,xt", [(2500, 5120, 64, "f32"), (700, 4640, 33, "bf16"), (4099, 2048, 17, "bf16"),
                                       (1100, 32, 3, "f32")])
 @pytest.mark.parametrize("where", ["first", "last", "all"])
