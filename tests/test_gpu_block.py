@@ -8,6 +8,8 @@ by a relative (D + 6) u plus (D u A)^2, and each further operation adds one u;
 another 2^-8 of itself away.  D follows from the kernel's layout: 8 V values
 per thread, 6 steps in the wave, W waves.
 """
+import ctypes
+
 import numpy as np
 import pytest
 import torch
@@ -636,6 +638,20 @@ def _every_form(act, yt, res, M, K, N):
         assert_close(f64(Y), ref, dy, yt, mode)
 
 
+FEW_TILES = [(0, 33, 2080, 544), (1, 197, 544, 1312), (2, 515, 1056, 1056), (3, 515, 4128, 2080), (3, 777, 4128, 1312)]
+
+
+@pytest.mark.parametrize("tile,M,K,N", FEW_TILES)
+@pytest.mark.parametrize("yt", ["bf16", "f32"])
+@pytest.mark.parametrize("res", [None, "bf16", "f32"])
+def test_every_form_of_the_few_token_tiles(tile, M, K, N, yt, res):
+    """Each few-token tile, ragged in both directions, with each output and residual type; the size
+    has to take the tile (a changed rule asks for another size)."""
+    size = {None: 0, "bf16": 2, "f32": 4}
+    assert _tile(M, N, K, 7, size[yt] + size[res]) == tile
+    _every_form({None: "gelu", "bf16": "silu", "f32": "none"}[res], yt, res, M, K, N)
+
+
 def test_epilogue_in_place_on_the_residual():
     rng = np.random.default_rng(4)
     for M, yt in ((9, "bf16"), (300, "f32"), (300, "bf16")):
@@ -662,6 +678,56 @@ def test_no_epilogue_is_the_dual_gemm():
         mg.mg_dual_gemm_ep(p, a, None, Z)
         v, t = decoded(p, a, 2100)
         assert_close(f64(Z), v, (1056 + 20) * U * t + 1e-37, "f32" if dt == torch.float32 else "bf16", "Y")
+
+
+def test_the_dual_gemm_and_its_form_with_an_epilogue():
+    """mg_dual_gemm and mg_dual_gemm_ep without an epilogue: the same bits where both take the
+    256x256 tiles, else sums of the same products in another order."""
+    rng = np.random.default_rng(16)
+    for M, K, N, big in ((8190, 1312, 2048, True), (2100, 1056, 1312, False), (33, 5120, 544, False)):
+        X, _ = rows(rng, M, K, "bf16")
+        p = _quant_plan(rng, K, N, 20, X)
+        a = mg.Act.empty(p.desc, M)
+        mg.mg_quantize_act(p, X, a)
+        _, t = decoded(p, a, M)
+        for dt in ("f32", "bf16"):
+            Y, Z = (torch.full((M, N), float("nan"), dtype=TYPES[dt], device="cuda") for _ in range(2))
+            mg.mg_dual_gemm(p, a, Y)
+            mg.mg_dual_gemm_ep(p, a, None, Z)
+            assert (_tile(M, N, K, 20, 4 if dt == "f32" else 2) < 0) == big
+            if big:
+                assert torch.equal(Y, Z)
+            other = 2.0 ** -8 * np.abs(f64(Y)) if dt == "bf16" else 0.0      # Y's own rounding, beside Z's
+            assert_close(f64(Z), f64(Y), 2 * (K + 20) * U * t + other + 1e-37, dt, "Y")
+
+
+def test_bf16_results_are_the_f32_results_rounded_once():
+    rng = np.random.default_rng(17)
+    for M, K, N in ((70, 1536, 96), (700, 5121, 0), (5000, 512, 2048), (300, 200, 0)):
+        X, _ = rows(rng, M, K, "bf16")
+        m = mg.Mod(**dict(zip(("scale", "shift"), modulation(rng, 1, K, "f32")[:2])))
+        H = {t: torch.empty(M, K, dtype=TYPES[t], device="cuda") for t in TYPES}
+        for h in H.values():
+            mg.mg_norm_mod(mg.Norm(), m, X, h)
+        assert torch.equal(H["f32"].bfloat16(), H["bf16"])
+        if N:
+            p = _quant_plan(rng, K, N, 9, X)
+            a = mg.Act.empty(p.desc, M)
+            mg.mg_quantize_act(p, X, a)
+            R, b = rows(rng, M, N, "f32")[0], vec(rng, N, "f32")
+            Y = {t: torch.empty(M, N, dtype=TYPES[t], device="cuda") for t in TYPES}
+            assert _tile(M, N, K, 9, 6) == _tile(M, N, K, 9, 8)          # the same order of sums
+            for y in Y.values():
+                mg.mg_dual_gemm_ep(p, a, mg.Epilogue(b, "gelu", None, R), y)
+            assert torch.equal(Y["f32"].bfloat16(), Y["bf16"])
+
+
+def _tile(M, N, K, k, nbytes):
+    """The GEMM's form by the rule that chooses it: 0 ... 3 the few-token tiles (32 x 32, 32 x 64,
+    64 x 64, 64 x 96), -1 the 256x256 tiles."""
+    f = mg.lib()["_ZN2mg8few_tileEliiii"]
+    f.argtypes, f.restype = [ctypes.c_int64] + 4 * [ctypes.c_int32], ctypes.c_int32
+    return f(M, N, K, k, nbytes)
 
 
 def test_zero_rows_launch_nothing():
