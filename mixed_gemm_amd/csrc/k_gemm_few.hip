@@ -13,9 +13,11 @@
 // ranges and read 0.  The waves' partial sums meet in LDS and are added in the
 // order of the waves, so a call's bits do not vary.
 //
-// Bound: one token, K = 5120 -> N = 13824 (37.6 MB of codes and scales) takes
-// 8.3 us and 13824 -> 5120 8.4 us inside a graph, 4.5 TB/s, against 3.2 us for
-// a 1568 x 1056 layer: the weights' way from memory.  With more tokens the
+// Bound: the weights' way into the CUs.  One token, K = 5120 -> N = 13824 (37.6
+// MB of codes and scales) takes 10.3 us and 13824 -> 5120 11.3 us where ten
+// plans take turns and the weights come from memory (3.7 and 3.3 TB/s), 8.3 and
+// 8.4 us with one plan, which the last-level cache holds, against 3.2 us for a
+// 1568 x 1056 layer; all inside a graph.  With more tokens the
 // operands' way into a CU (few_tile).  Fewer registers pay more than more
 // loads in flight: 4 waves with one or two half-windows leave room for two to
 // three workgroups on a CU, whose starts and joins overlap the others' K loops
@@ -302,7 +304,7 @@ hipError_t run_few(int tile, const FewArgs& a, hipStream_t st) {
 // residual in f32), whose choices lie 1.1 % above the best tile's time, 30 % at
 // worst; without k and the output's bytes 7.6 %, 150 % at worst (11496 tokens,
 // 416 -> 7552: 75 us with 256x256 tiles, 190 us with (2, 3)).  Measured against the 256x256 tiles, gate
-// and residual in bf16: 5120 -> 13824 at 1, 64, 256, 384 tokens 8.3, 10.7, 24.5,
+// and residual in bf16, one plan in the last-level cache: 5120 -> 13824 at 1, 64, 256, 384 tokens 8.3, 10.7, 24.5,
 // 32.0 (33.4, 33.8, 35.6, 37.6), 13824 -> 5120 at 1, 64, 256, 1024 tokens 8.4,
 // 12.7, 22.9, 67.9 (72.9, 73.5, 74.8, 77.0), 1568 -> 1056 at 777 tokens 6.6
 // (19.6).

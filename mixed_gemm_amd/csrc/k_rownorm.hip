@@ -14,7 +14,8 @@
 // Rows may start at any element and have any width from 8 on: loads are
 // unaligned 16-byte loads, and a thread at the row's end holds the row's last
 // 8 channels, so that no load needs a branch; those of them that the thread
-// before holds too count as 0 in the sums and are not stored.
+// before holds too count as 0 in the sums, and are stored by both with the same
+// value, or by the thread before alone where outputs and inputs share memory.
 #include <type_traits>
 
 #include "mg_block.h"
@@ -416,12 +417,12 @@ struct RowShape {
 // and Y (YT void: no residual step).
 //
 // Bound: memory, each row read and written once.  Norm with modulation of
-// 32760 x 5120, f32 in, bf16 out (1006 MB): 172-183 us, 5.5-5.8 TB/s (a 1 GiB
-// copy: 5.1); bf16 in 131 us, 5.1.  Gated residual with the next norm of
-// 75600 x 5120, f32 stream, bf16 block output (4.65 GB): 859 us, 5.4; bf16
-// stream 562 us, 5.5.  10000 x 13824 f32 316 us, 5.2.  9973 x 2049 bf16 with a
-// norm after the block and padding rows (164 MB) 51 us, 3.2: rows at odd
-// addresses and two exchanges a row.  One row: 3.8-4.0 us, the
+// 32760 x 5120, f32 in, bf16 out (1006 MB): 172 us, 5.8 TB/s (a 1 GiB copy:
+// 5.1); bf16 in 123 us, 5.4.  Gated residual with the next norm of
+// 75600 x 5120, f32 stream, bf16 block output (4.65 GB): 872 us, 5.3; bf16
+// stream 545 us, 5.7.  10000 x 13824, f32 stream, 322 us, 5.2.  9973 x 2049 bf16
+// with a norm after the block and padding rows (164 MB) 51 us, 3.2: rows at odd
+// addresses and two exchanges a row.  One row: 3.8-4.2 us, the
 // launch and one trip to memory.  Reading a row twice (statistics, then the
 // result) would cost half as much again; two rows ahead instead of one
 // measured no gain, since the waves on a CU already fill its path to memory.
@@ -578,10 +579,11 @@ row_kernel(RowArgs a, RowSpan span) {
 // Rows of 8 to 256 channels, heads as a norm of queries and keys has them: 16
 // or 32 lanes take a row, a wave 4 or 2 (a wave each leaves most lanes idle:
 // residual bf16 of 75600 rows, 65 wide 46 us against 12, 129 wide 47 us against
-// 20, 256 wide 46 us against 32).  No barrier, one row ahead in flight.  The
-// sums are row_kernel's of one wave, so the bits are.  Bound: memory where rows
-// fill the lanes (75600 x 100, residual bf16, 12.2 us, 4.9 TB/s; norm of f32 into
-// bf16 8.9 us, 5.1), else the instructions of a row.
+// 20, 256 wide 46 us against 32, in the last-level cache).  No barrier, one row
+// ahead in flight.  The sums are row_kernel's of one wave, so the bits are.
+// Bound: memory where rows fill the lanes (75600 x 256, residual bf16, 32 us, 4.8
+// TB/s; x 100 15-16 us, 3.8, from the cache 12.2; norm of f32 into bf16 11.5 us,
+// 3.9), else the instructions of a row.
 struct NarrowThread {
     int at[1];                      // channel of the lane's first element
     __device__ __forceinline__ void load8(const void* p, int64_t row, int32_t dtype, int v, float (&x)[8]) const {
@@ -929,7 +931,7 @@ __device__ __forceinline__ void flush_unit(const NormQuantArgs& g, int64_t r0, i
 // coefficients' loads, the division and the blocks' maxima one after the other:
 // one row of 5120 7.7 us, 256 rows 8.9 us.  From more rows on the form below
 // is faster (32760 x 5120 f32: 352 us here); its 10 windows a row are the most
-// that registers hold, so wider rows stay here (8000 x 13824 bf16 112 us, 2.5
+// that registers hold, so wider rows stay here (8000 x 13824 bf16 113 us, 2.5
 // TB/s).
 template <int V, typename XT>
 __global__ void __launch_bounds__(V <= 4 ? 512 : 1024) __attribute__((amdgpu_waves_per_eu(V > 4 ? 4 : V == 4 ? 2 : V == 2 ? 3 : 4)))
@@ -1034,8 +1036,8 @@ norm_quant_kernel(NormQuantArgs g, int R) {
 // last can be partial.  The sums are row_kernel's (those of its W waves), so
 // the bits are.
 // Bound: memory and the arithmetic of the quantize step together: 32760 x 5120
-// f32 (755 MB) 162-170 us, 4.4-4.7 TB/s; bf16 (420 MB, 83 us at a copy's rate)
-// 128 us, 3.3, where the arithmetic is the longer part.  A row per W waves with
+// f32 (764 MB) 161-167 us, 4.6-4.7 TB/s; bf16 (428 MB, 84 us at a copy's rate)
+// 123 us, 3.5, where the arithmetic is likely the longer part.  A row per W waves with
 // the constants in registers took 352 us and 322 us, dividing the outlier
 // channels with the others 238 us and 198 us.
 template <int V>
