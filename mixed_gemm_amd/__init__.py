@@ -1340,17 +1340,18 @@ class F8Work:
 
 @_on_stream
 def f8_backward(p: F8Plan, saved: F8, dY: torch.Tensor, dX: torch.Tensor | None = None,
-                dW: torch.Tensor | None = None, fmt: str = "e4m3", work: F8Work | None = None,
+                dW: torch.Tensor | None = None, fmt: str | None = None, work: F8Work | None = None,
                 need: tuple = (True, True), stream=None):
     """Gradients of f8_forward (without an epilogue) with respect to X and W, from
     the gradient dY [M][N] and the 8-bit checkpoint of X; quantization counts as
     the identity.  dX and dW are made in bf16 and f32 where not given; `need`
-    leaves one out (None is returned for it)."""
+    leaves one out (None is returned for it).  fmt is dY's 8-bit format: that of
+    `work` where given (another one is refused), else "e4m3"."""
     N, K, M = p.w.rows, p.w.cols, dY.shape[0]
     _f8(saved, "saved", M, K, "e4m3")
     if work is None:
-        work = F8Work.empty(p, M, fmt)
-    _f8(work.dy, "work.dy", M, N)
+        work = F8Work.empty(p, M, "e4m3" if fmt is None else fmt)
+    _f8(work.dy, "work.dy", M, N, fmt)
     if need[0]:
         _need(p.wt is not None, "the plan has no transposed weight: make it with backward=True")
         if dX is None:
@@ -1461,17 +1462,19 @@ def gated_ffn_forward(ffn: GatedFFN, X: torch.Tensor, saved: GatedSaved | None =
 @_on_stream
 def gated_ffn_backward(ffn: GatedFFN, saved: GatedSaved, dY: torch.Tensor, dX: torch.Tensor | None = None,
                        dWg: torch.Tensor | None = None, dWu: torch.Tensor | None = None,
-                       dWd: torch.Tensor | None = None, fmt: str = "e4m3", work: GatedWork | None = None, stream=None):
+                       dWd: torch.Tensor | None = None, fmt: str | None = None, work: GatedWork | None = None,
+                       stream=None):
     """Gradients (dX, dWg, dWu, dWd) of gated_ffn_forward (without an epilogue),
     from dY [M][N] and what the forward pass put away; quantization counts as the
     identity.  Made in bf16 (dX) and f32 where not given.  fmt is the gradients'
-    8-bit format (that of `work` where given)."""
+    8-bit format: that of `work` where given (another one is refused), else "e4m3"."""
     _need(ffn.w13t is not None and ffn.wdt is not None, "the block has no transposed weights: make it with backward=True")
     M, dev = dY.shape[0], dY.device
     _f8(saved.x, "saved.x", M, ffn.K)
     if work is None:
-        work = GatedWork.empty(ffn, M, fmt)
+        work = GatedWork.empty(ffn, M, "e4m3" if fmt is None else fmt)
     _need(work.back is not None, "work is for the forward pass alone: make it with fmt")
+    _need(fmt is None or fmt == work.fmt, f"work is for gradients in {work.fmt}, not {fmt}")
     _need(work.M == M, f"work is for {work.M} rows, dY has {M}")
     if dX is None:
         dX = torch.empty((M, ffn.K), dtype=torch.bfloat16, device=dev)
