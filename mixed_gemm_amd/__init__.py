@@ -1338,6 +1338,15 @@ class F8Work:
         return F8Work(F8.empty(M, N, fmt, dev), F8.empty(N, m, fmt, dev), F8.empty(K, m, device=dev))
 
 
+def _gradient(t: torch.Tensor | None, name: str, rows: int, cols: int, dtype: torch.dtype, like: torch.Tensor):
+    """An output of a backward pass: `t` where given, checked before the first launch, else a new one."""
+    if t is None:
+        return torch.empty((rows, cols), dtype=dtype, device=like.device)
+    _dense(t, name, rows, cols)
+    _dtype(t)
+    return t
+
+
 @_on_stream
 def f8_backward(p: F8Plan, saved: F8, dY: torch.Tensor, dX: torch.Tensor | None = None,
                 dW: torch.Tensor | None = None, fmt: str | None = None, work: F8Work | None = None,
@@ -1354,10 +1363,9 @@ def f8_backward(p: F8Plan, saved: F8, dY: torch.Tensor, dX: torch.Tensor | None 
     _f8(work.dy, "work.dy", M, N, fmt)
     if need[0]:
         _need(p.wt is not None, "the plan has no transposed weight: make it with backward=True")
-        if dX is None:
-            dX = torch.empty((M, K), dtype=torch.bfloat16, device=dY.device)
-    if need[1] and dW is None:
-        dW = torch.empty((N, K), dtype=torch.float32, device=dY.device)
+        dX = _gradient(dX, "dX", M, K, torch.bfloat16, dY)
+    if need[1]:
+        dW = _gradient(dW, "dW", N, K, torch.float32, dY)
     if M == 0:
         if need[1]:
             dW.zero_()
@@ -1469,17 +1477,19 @@ def gated_ffn_backward(ffn: GatedFFN, saved: GatedSaved, dY: torch.Tensor, dX: t
     identity.  Made in bf16 (dX) and f32 where not given.  fmt is the gradients'
     8-bit format: that of `work` where given (another one is refused), else "e4m3"."""
     _need(ffn.w13t is not None and ffn.wdt is not None, "the block has no transposed weights: make it with backward=True")
-    M, dev = dY.shape[0], dY.device
-    _f8(saved.x, "saved.x", M, ffn.K)
+    M = dY.shape[0]
+    for x, n, cols in ((saved.x, "saved.x", ffn.K), (saved.gu, "saved.gu", 2 * _up128(ffn.F)), (saved.h, "saved.h", ffn.F)):
+        _f8(x, n, M, cols)
     if work is None:
         work = GatedWork.empty(ffn, M, "e4m3" if fmt is None else fmt)
     _need(work.back is not None, "work is for the forward pass alone: make it with fmt")
     _need(fmt is None or fmt == work.fmt, f"work is for gradients in {work.fmt}, not {fmt}")
     _need(work.M == M, f"work is for {work.M} rows, dY has {M}")
-    if dX is None:
-        dX = torch.empty((M, ffn.K), dtype=torch.bfloat16, device=dev)
-    f = lambda t, r, c: torch.empty((r, c), dtype=torch.float32, device=dev) if t is None else t  # noqa: E731
-    dWg, dWu, dWd = f(dWg, ffn.F, ffn.K), f(dWu, ffn.F, ffn.K), f(dWd, ffn.N, ffn.F)
+    dX = _gradient(dX, "dX", M, ffn.K, torch.bfloat16, dY)
+    dWg = _gradient(dWg, "dWg", ffn.F, ffn.K, torch.float32, dY)
+    dWu = _gradient(dWu, "dWu", ffn.F, ffn.K, torch.float32, dY)
+    dWd = _gradient(dWd, "dWd", ffn.N, ffn.F, torch.float32, dY)
+    _need(dWg.dtype == dWu.dtype, "dWg and dWu must have the same type")
     if M == 0:
         for t in (dWg, dWu, dWd):
             t.zero_()

@@ -75,3 +75,64 @@ def test_the_workspace_has_the_format(nothing_runs, fmt, given):
         mg.f8_backward(p, saved, dY, work=work, **kw)
     with pytest.raises(AssertionError, match="went through"):
         mg.gated_ffn_backward(ffn, kept, dy, work=gwork, **kw)
+
+
+def wrong(rows, cols):
+    """Outputs that do not fit [rows][cols], with what the refusal says."""
+    return [(on(rows + 1, cols), "must be"), (on(rows, cols + 32), "must be"), (on(rows, cols, dtype=torch.float16), "dtype"),
+            (on(cols, rows).t(), "contiguous"), (torch.zeros(rows, cols), "device")]
+
+
+@pytest.mark.parametrize("which", [0, 1])
+@pytest.mark.parametrize("i", range(5))
+def test_linear_gradients_are_checked_first(nothing_runs, which, i):
+    """An output that does not fit is refused before anything runs."""
+    p, saved, dY, work = linear()
+    out, says = wrong(*((M, K), (N, K))[which])[i]
+    nothing_runs()
+    for need in ((True, True), (which == 0, which == 1)):
+        with pytest.raises(ValueError, match=says):
+            mg.f8_backward(p, saved, dY, **{("dX", "dW")[which]: out}, work=work, need=need)
+
+
+@pytest.mark.parametrize("which", range(4))
+@pytest.mark.parametrize("i", range(5))
+def test_gated_gradients_are_checked_first(nothing_runs, which, i):
+    ffn, saved, dY, work = gated()
+    out, says = wrong(*((M, K), (F, K), (F, K), (N, F))[which])[i]
+    nothing_runs()
+    with pytest.raises(ValueError, match=says):
+        mg.gated_ffn_backward(ffn, saved, dY, **{("dX", "dWg", "dWu", "dWd")[which]: out}, work=work)
+
+
+def test_gated_weight_gradients_of_two_types(nothing_runs):
+    ffn, saved, dY, work = gated()
+    nothing_runs()
+    with pytest.raises(ValueError, match="type"):
+        mg.gated_ffn_backward(ffn, saved, dY, dWg=on(F, K), dWu=on(F, K, dtype=torch.bfloat16), work=work)
+
+
+def test_gradients_of_no_rows_are_checked(nothing_runs):
+    """Without rows the weight gradients are cleared: only ones that fit."""
+    p, x, dY = mg.F8Plan(f8(N, K), f8(K, N)), f8(0, K), on(0, N)
+    work = mg.F8Work(f8(0, N), f8(N, 32), f8(K, 32))
+    ffn, saved = gated()[0], mg.GatedSaved(f8(0, K), f8(0, 512), f8(0, F))
+    gwork = mg.GatedWork(f8(0, K), f8(0, F), on(0, dtype=torch.uint8), "e4m3", {})
+    nothing_runs()
+    for kw in (dict(dW=on(3, 3) + 1), dict(dX=on(1, K))):
+        with pytest.raises(ValueError, match="must be"):
+            mg.f8_backward(p, x, dY, work=work, **kw)
+    for kw in (dict(dWg=on(3, 3)), dict(dWd=on(F, N)), dict(dX=on(1, K))):
+        with pytest.raises(ValueError, match="must be"):
+            mg.gated_ffn_backward(ffn, saved, dY, work=gwork, **kw)
+    dW = on(N, K) + 1
+    assert not mg.f8_backward(p, x, dY, dX=on(0, K), dW=dW, work=work)[1].any()
+
+
+@pytest.mark.parametrize("name", ["gu", "h"])
+def test_gated_saved_of_another_block(nothing_runs, name):
+    ffn, saved, dY, work = gated()
+    setattr(saved, name, f8(M, 256))
+    nothing_runs()
+    with pytest.raises(ValueError, match=f"saved.{name}"):
+        mg.gated_ffn_backward(ffn, saved, dY, work=work)
