@@ -678,6 +678,8 @@ class Epilogue:
             _need(bias.dim() == 1 and bias.is_cuda and bias.is_contiguous(), "bias must be a contiguous device vector")
         ldr = _rows(residual, "residual")[1] if residual is not None else 0
         self.bias, self.gate, self.residual = bias, gate, residual
+        tensors = (bias, residual) if gate is None else (bias, residual, *gate.tensors[2:])     # of gate: rows and index
+        self.devs = {t.get_device() for t in tensors if t is not None}
         self.c = mg_epilogue(_ptr(bias), None if residual is None else residual.data_ptr(),
                              None if gate is None else gate.ref, ldr, MG_F32 if bias is None else _dtype(bias),
                              MG_F32 if residual is None else _dtype(residual), ACTS[act], 0)
@@ -826,6 +828,15 @@ def _here(t: torch.Tensor, name: str) -> None:
         raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
 
 
+def _f8_epilogue(ep: Epilogue, M: int, N: int) -> None:
+    """Its sizes, and its tensors on the current device."""
+    ep.check(M, N)
+    dev = _device()
+    for d in ep.devs:
+        if d != dev:
+            raise ValueError(f"the epilogue has a tensor on device {d}, the current device is {dev}")
+
+
 def _f8(x, name: str, rows: int | None = None, cols: int | None = None, fmt: str | None = None) -> None:
     if not isinstance(x, F8):
         raise ValueError(f"{name} must be an F8")
@@ -915,7 +926,7 @@ def mg_f8_gemm(a: F8, w: F8, ep: Epilogue | None, Y: torch.Tensor, stream=None) 
     _f8(w, "w", None, a.cols)
     y = _dense(Y, "Y", a.rows, w.rows)
     if ep is not None:
-        ep.check(a.rows, w.rows)
+        _f8_epilogue(ep, a.rows, w.rows)
     code = lib().mg_f8_gemm(a.ref, w.ref, _ref(ep), y, _dtype(Y), _stream(stream))
     if code:
         _check(code)
@@ -929,7 +940,7 @@ def mg_f8_forward(X: torch.Tensor, act: F8, w: F8, ep: Epilogue | None, Y: torch
     _f8(w, "w", None, act.cols)
     y = _dense(Y, "Y", M, w.rows)
     if ep is not None:
-        ep.check(M, w.rows)
+        _f8_epilogue(ep, M, w.rows)
     code = lib().mg_f8_forward(X.data_ptr(), _dtype(X), ld, act.ref, int(bool(save)), w.ref, _ref(ep), y, _dtype(Y),
                                _stream(stream))
     if code:
@@ -996,7 +1007,7 @@ def mg_gated_forward(X: torch.Tensor, x: F8, w13: F8, act: str, h: F8, gu: F8 | 
         _f8(gu, "gu", M, 2 * Fp)
     y = _dense(Y, "Y", M, wd.rows)
     if ep is not None:
-        ep.check(M, wd.rows)
+        _f8_epilogue(ep, M, wd.rows)
     sc = _scratch(scratch, mg_gated_scratch_bytes(M, h.cols, x.cols)[0])
     code = lib().mg_gated_forward(X.data_ptr(), _dtype(X), ld, x.ref, w13.ref, ACTS[act], h.ref, _ref(gu), sc, wd.ref,
                                   _ref(ep), y, _dtype(Y), _stream(stream))

@@ -136,3 +136,44 @@ def test_gated_saved_of_another_block(nothing_runs, name):
     nothing_runs()
     with pytest.raises(ValueError, match=f"saved.{name}"):
         mg.gated_ffn_backward(ffn, saved, dY, work=work)
+
+
+class On1(On0):
+    """A host tensor that says it is on device 1."""
+
+    def get_device(self):
+        return 1
+
+
+def far(*shape, dtype=torch.float32):
+    return torch.zeros(*shape, dtype=dtype).as_subclass(On1)
+
+
+EPILOGUES = {
+    "bias": lambda: mg.Epilogue(bias=far(N)),
+    "residual": lambda: mg.Epilogue(residual=far(M, N)),
+    "gate": lambda: mg.Epilogue(gate=mg.Mod(gate=far(1, N))),
+    "gate index": lambda: mg.Epilogue(gate=mg.Mod(gate=on(2, N), index=far(M, dtype=torch.int32))),
+    "gate index alone": lambda: mg.Epilogue(gate=mg.Mod(rows=2, index=far(M, dtype=torch.int32))),
+    "one of several": lambda: mg.Epilogue(bias=on(N), gate=mg.Mod(gate=on(1, N)), residual=far(M, N)),
+}
+
+
+@pytest.mark.parametrize("kind", sorted(EPILOGUES))
+def test_epilogue_on_another_device(nothing_runs, kind):
+    """Kernels run on the current device and would read what the epilogue points at."""
+    ep = EPILOGUES[kind]()
+    p, x, ffn, work = mg.F8Plan(f8(N, K)), f8(M, K), *(gated()[i] for i in (0, 3))
+    nothing_runs()
+    for call in (lambda: mg.mg_f8_gemm(x, p.w, ep, on(M, N)), lambda: mg.f8_forward(p, on(M, K), ep, x, on(M, N)),
+                 lambda: mg.gated_ffn_forward(ffn, on(M, K), Y=on(M, N), work=work, ep=ep)):
+        with pytest.raises(ValueError, match="device"):
+            call()
+
+
+def test_epilogue_on_the_current_device(nothing_runs):
+    ep = mg.Epilogue(on(N), "silu", mg.Mod(gate=on(2, N), index=on(M, dtype=torch.int32)), on(M, N))
+    p, x = mg.F8Plan(f8(N, K)), f8(M, K)
+    nothing_runs()
+    with pytest.raises(AssertionError, match="went through"):
+        mg.mg_f8_gemm(x, p.w, ep, on(M, N))
