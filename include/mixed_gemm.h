@@ -451,7 +451,9 @@ int mg_forward_ep(const mg_plan* p, const void* X, int32_t dtype, int64_t M, con
  * and the scale costs no precision.  A weight has one c for each tile of
  * 128 x 128 (repeated on the tile's rows), so its transpose holds the same
  * codes.  A block (a weight: a tile) that holds a NaN or an infinity is NaN throughout,
- * and so is everything computed from it.
+ * and so is everything computed from it.  Magnitudes from 2^128 (1 - 2^-5) on (E5M2: 1 -
+ * 2^-4) are finite in f32 but round to 2^128, which is not: they come back as
+ * infinities, and count as such in a transpose.
  *
  * cols is a multiple of 32, rows any number; q and s are device buffers of
  * mg_f8_bytes bytes, s [..] u32:
