@@ -529,8 +529,8 @@ int mg_f8_gemm(const mg_f8* a, const mg_f8* w, const mg_epilogue* e, void* Y, in
 
 /* mg_f8_quantize of X into act (E4M3), then mg_f8_gemm of it.  save 1 leaves
  * X's codes in act, for the backward pass; with save 0 act is workspace, and a
- * few rows (up to 16, and 28 K values) are quantized inside the product, in
- * one launch: the same codes, sums in another order. */
+ * few rows (at most 16 and 28 K values, fewer where N is large) are quantized
+ * inside the product, in one launch: the same codes, sums in another order. */
 int mg_f8_forward(const void* X, int32_t dtype, int64_t ldx, const mg_f8* act, int32_t save, const mg_f8* w,
                   const mg_epilogue* e, void* Y, int32_t y_dtype, hipStream_t stream);
 

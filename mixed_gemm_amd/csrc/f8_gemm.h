@@ -40,8 +40,8 @@ struct F8DirectArgs {
 };
 int f8_direct_rows(int32_t K);
 // whether a layer, or the gated block, is faster so than with its rows quantized first
-bool f8_direct_pays(int64_t M, int32_t K);
-bool f8_direct_pays_gated(int64_t M, int32_t K, int32_t F);
+bool f8_direct_pays(int64_t M, int32_t K, int32_t N);
+bool f8_direct_pays_gated(int64_t M, int32_t K, int32_t F, int32_t N);
 hipError_t launch_f8_direct(F8DirectArgs a, int32_t x_dtype, int32_t y_dtype, bool gated, hipStream_t st);
 
 // an epilogue that changes nothing

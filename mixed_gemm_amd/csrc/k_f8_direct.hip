@@ -240,17 +240,40 @@ int f8_direct_rows(int32_t K) {
     return fit < kDirRows ? fit : kDirRows;
 }
 
-// Every workgroup quantizes all rows, so the two launches win once that is more
-// than a launch's latency.  Direct against two launches, in a graph, weights from
-// memory: 5120 -> 13824 1 row 15.0 us, 17.0; 3 rows 16.8, 17.4; 4 rows 17.7, 17.4; 8
-// rows 21.2, 17.5; 13824 -> 5120 2 rows 19.0, 20.4; 3 rows 21.1, 20.3; 5120 -> 5120 4
-// rows 10.2, 10.8; 8 rows 12.6, 10.8; 2048 -> 8192 16 rows 9.5, 9.6; 1568 -> 1056 16
-// rows 6.5, 7.0.  The gated block saves two launches: 5120 -> 13824 1 row 43.4, 50.1; 4
-// rows 50.6, 51.1.
-bool f8_direct_pays(int64_t M, int32_t K) { return M <= f8_direct_rows(K) && M * (f8_slices(K) / 4) <= 224; }
+// Column tiles of the last product for each CU, at least 1.
+static double tiles_per_cu(int32_t N) {
+    const double t = (N + 31) / 32 / (double)device_cu_count();
+    return t > 1.0 ? t : 1.0;
+}
 
-bool f8_direct_pays_gated(int64_t M, int32_t K, int32_t F) {
-    return M <= f8_direct_rows(K) && M <= f8_direct_rows(F) && M * (f8_slices(K) / 4 + f8_slices(F) / 4) <= 600;
+// Every workgroup quantizes all rows, so the two launches win once that is more
+// than a launch's latency, and the sooner the more workgroups a CU runs.  Up to
+// three rows of 2048 channels or more stay: their weights' way is the time, and
+// the direct kernel streams them faster.  Direct against two launches, in a graph,
+// weights from memory: 5120 -> 13824 1 row 15.1 us, 17.1; 3 rows 16.9, 17.4; 4 rows
+// 17.9, 17.5; 5 rows 18.8, 17.5; 5120 -> 55296 1 row 52, 58; 5 rows 60, 56; 13824 -> 5120
+// 2 rows 19.1, 20.3; 3 rows 21.1, 20.3; 5120 -> 5120 4 rows 10.1, 10.7; 8 rows 12.6, 10.8; 2048
+// -> 8192 14 rows 9.0, 9.2; 1024 -> 1056 16 rows 5.2, 6.2; 1024 -> 13824 12 rows 7.9, 8.0;
+// 16 rows 8.5, 8.1; 1024 -> 55296 1 row 16.0, 14.7; 16 rows 24.4, 15.8; 1024 -> 131072 16
+// rows 49.6, 29.9.  Of 133 such calls (K 1024 to 13824, N 1056 to 131072) the rule
+// takes the slower one, by 4 to 7 %, at 5120 -> 8192 5 rows, 13824 -> 8192 and -> 27648 2
+// rows, 5120 -> 27648 3 rows, and by less elsewhere.
+bool f8_direct_pays(int64_t M, int32_t K, int32_t N) {
+    const int64_t units = f8_slices(K) / 4;
+    if (M > f8_direct_rows(K) || M * units > 224) return false;
+    return (M <= 3 && units >= 16) || (double)(M * units + 32) * tiles_per_cu(N) <= 264.0;
+}
+
+// The gated block saves two launches and quantizes twice.  Direct against its
+// steps apart: 5120 -> 13824 -> 5120 1 row 47.0, 49.9; 3 rows 48.8, 50.6; 4 rows 51.0, 50.6; 1024
+// -> 4096 -> 1024 9 rows 17.1, 17.3; 13 rows 19.5, 17.4; 5120 -> 5120 -> 5120 5 rows 27.2, 26.6; 7 rows
+// 30.0, 26.9; 5120 -> 1024 -> 5120 11 rows 22.3, 18.7; 2048 -> 2048 -> 55296 3 rows 31.3, 34.3; 16 rows
+// 50.0, 36.0.  Of 70 such blocks the rule takes the slower form, by 9 %, at 5120
+// -> 1024 -> 5120 8 rows, and by 2 % at most elsewhere.
+bool f8_direct_pays_gated(int64_t M, int32_t K, int32_t F, int32_t N) {
+    const int64_t units = f8_slices(K) / 4 + f8_slices(F) / 4;
+    if (M > f8_direct_rows(K) || M > f8_direct_rows(F) || M * units > 600) return false;
+    return M <= 3 || (double)(M * units) * tiles_per_cu(N) <= 470.0;
 }
 
 hipError_t launch_f8_direct(F8DirectArgs a, int32_t x_dtype, int32_t y_dtype, bool gated, hipStream_t st) {

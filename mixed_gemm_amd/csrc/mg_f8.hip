@@ -261,7 +261,7 @@ int mg_f8_forward(const void* X, int32_t dtype, int64_t ldx, const mg_f8* act, i
     if (g.M == 0) return MG_OK;
     if (int c = check_matrix(X, dtype, ldx, x.rows, x.cols, "X")) return c;
     if (int c = check_grid(x.rows, x.cols, "act")) return c;
-    if (!save && f8_direct_pays(g.M, g.K)) {
+    if (!save && f8_direct_pays(g.M, g.K, g.N)) {
         const F8DirectArgs d{X, ldx, g.Wq, g.Ws, Y, (int32_t)g.M, g.N, g.K, 0, 0, g.ep, 0, 0};
         return hip_status(launch_f8_direct(d, dtype, y_dtype, false, stream), "mg_f8_forward");
     }
@@ -323,7 +323,7 @@ int mg_gated_forward(const void* X, int32_t dtype, int64_t ldx, const mg_f8* x, 
     if (int c = check_grid(a.rows, a.cols, "x")) return c;
     if (!fused_up(a, o, s)) MG_CHECK_PTR(scratch, "scratch");
     const char* where = "mg_gated_forward";
-    if (gu == nullptr && f8_direct_pays_gated(a.rows, a.cols, o.cols)) {
+    if (gu == nullptr && f8_direct_pays_gated(a.rows, a.cols, o.cols, g.N)) {
         const int32_t M = (int32_t)a.rows, F = o.cols;
         const F8DirectArgs up{X, ldx, w.q, w.s, scratch, M, (int32_t)w.rows, a.cols, F, act, no_epilogue(), 0, 0};
         if (int c = hip_status(launch_f8_direct(up, dtype, MG_F32, true, stream), where)) return c;

@@ -30,10 +30,16 @@ def fused(M: int, F: int, C: int) -> tuple:
     return tuple(bool(f(M, F, C, what)) for what in range(3))
 
 
-def gated_direct(M: int, K: int, F: int) -> bool:
-    """Whether the gated block goes straight from its activations."""
-    f = _symbol("_ZN2mg20f8_direct_pays_gatedElii", [ctypes.c_int64] + 2 * [ctypes.c_int32], ctypes.c_bool)
-    return bool(f(M, K, F))
+def linear_direct(M: int, K: int, N: int) -> bool:
+    """Whether a layer goes straight from its activations."""
+    f = _symbol("_ZN2mg14f8_direct_paysElii", [ctypes.c_int64] + 2 * [ctypes.c_int32], ctypes.c_bool)
+    return bool(f(M, K, N))
+
+
+def gated_direct(M: int, K: int, F: int, N: int) -> bool:
+    """Whether the gated block does."""
+    f = _symbol("_ZN2mg20f8_direct_pays_gatedEliii", [ctypes.c_int64] + 3 * [ctypes.c_int32], ctypes.c_bool)
+    return bool(f(M, K, F, N))
 
 
 # (tile, output, M, K, N): ragged in both directions, K over several scale windows where it can be; the

@@ -18,13 +18,13 @@ from tests.test_gpu_f8 import TYPES, assert_close, assert_q, f64, hidden, produc
 
 # (rows, K, F, N, whether they go direct): F with and without a remainder, several blocks of K and of F
 SIZES = [(1, 64, 32, 32, True), (1, 288, 416, 96, True), (2, 1056, 1056, 160, True), (4, 288, 1184, 544, True),
-         (7, 1056, 544, 64, True), (16, 544, 1056, 160, True), (12, 4128, 2080, 96, True), (13, 4128, 2080, 96, False),
-         (16, 2080, 2848, 64, False), (17, 288, 416, 96, False)]
+         (7, 1056, 544, 64, True), (16, 544, 1056, 160, True), (9, 4128, 2080, 96, True), (13, 4128, 2080, 96, False),
+         (16, 2080, 2848, 64, False), (16, 288, 544, 32800, False), (3, 288, 544, 32800, True), (17, 288, 416, 96, False)]
 
 
 def test_sizes_take_their_path():
-    for M, K, F, _, direct in SIZES:
-        assert gated_direct(M, K, F) == direct
+    for M, K, F, N, direct in SIZES:
+        assert gated_direct(M, K, F, N) == direct, (M, K, F, N)
 
 
 def hidden_close(h, x, wg, wu, act):
