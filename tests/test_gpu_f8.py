@@ -393,7 +393,7 @@ def test_epilogue(M, K, N, act, out):
     assert_close(f64(y), ref, np.abs(gr) * bound + 2.0 ** -22 * (np.abs(ref) + np.abs(gr * a)), out)
 
 
-# ------------------------------------------- sizes of the 256 x 256 tiles
+# ------------------------------------------------ sizes of many tiles
 
 def values_on_gpu(x):
     """The values of an F8 in f64 (by the library's own dequantize, tested above)."""
@@ -434,7 +434,7 @@ def big_q(x, ref, bound, what):
     assert not bad.any(), f"{what}: {int(bad.sum())} of {bad.numel()} off, first at {bad.nonzero()[0].tolist()}"
 
 
-# 256 x 256, 128 x 128 (ragged, one K block, several rounds) and small tiles, as the sizes ask for them
+# 128 x 128 (ragged, one K block, several rounds) and small tiles, as the sizes ask for them; every tile: test_gpu_f8_forms.py
 BIG = [(2304, 800, 1568), (1003, 2048, 2080), (2000, 32, 4064), (6700, 352, 1536), (500, 4096, 1056), (4000, 32, 2080), (4000, 96, 2080), (300, 640, 16416), (8200, 1568, 1056), (33000, 160, 32), (8192, 544, 1024)]
 
 
