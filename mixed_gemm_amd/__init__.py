@@ -1490,7 +1490,7 @@ def gated_ffn_backward(ffn: GatedFFN, saved: GatedSaved, dY: torch.Tensor, dX: t
     _need(ffn.w13t is not None and ffn.wdt is not None, "the block has no transposed weights: make it with backward=True")
     M = dY.shape[0]
     for x, n, cols in ((saved.x, "saved.x", ffn.K), (saved.gu, "saved.gu", 2 * _up128(ffn.F)), (saved.h, "saved.h", ffn.F)):
-        _f8(x, n, M, cols)
+        _f8(x, n, M, cols, "e4m3")
     if work is None:
         work = GatedWork.empty(ffn, M, "e4m3" if fmt is None else fmt)
     _need(work.back is not None, "work is for the forward pass alone: make it with fmt")

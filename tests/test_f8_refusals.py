@@ -138,6 +138,15 @@ def test_gated_saved_of_another_block(nothing_runs, name):
         mg.gated_ffn_backward(ffn, saved, dY, work=work)
 
 
+@pytest.mark.parametrize("name,cols", [("x", K), ("gu", 512), ("h", F)])
+def test_gated_saved_in_another_format(nothing_runs, name, cols):
+    ffn, saved, dY, work = gated()
+    setattr(saved, name, f8(M, cols, "e5m2"))
+    nothing_runs()
+    with pytest.raises(ValueError, match=f"saved.{name} must be e4m3"):
+        mg.gated_ffn_backward(ffn, saved, dY, work=work)
+
+
 class On1(On0):
     """A host tensor that says it is on device 1."""
 
