@@ -12,7 +12,7 @@ import torch
 
 import mixed_gemm_amd as mg
 from oracle import f8 as of8
-from tests.f8_forms import gated_direct
+from tests.f8_forms import gated_direct, linear_direct
 from tests.f8_util import value
 from tests.test_gpu_f8 import TYPES, assert_close, assert_q, f64, hidden, product, rows
 
@@ -92,3 +92,41 @@ def test_exchanged_groups_would_show():
     with pytest.raises(AssertionError, match="off"):
         hidden_close(right, x, np.concatenate([wg[:32], wu[32:]]), np.concatenate([wu[:32], wg[32:]]), "silu")
     hidden_close(right, x, wg, wu, "silu")
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("M", [1, 3])
+def test_few_rows_replayed(M):
+    """A layer and a block straight from their activations, captured: replays with new inputs, between eager
+    calls of the same workspace, give the eager bits."""
+    K, F, N = 1056, 544, 160
+    W, _ = weights(K, F, N)
+    plan, ffn = mg.f8_plan(W[0]), mg.gated_ffn(*W, "silu")
+    assert linear_direct(M, K, F) and gated_direct(M, K, F, N)
+    act, work = mg.F8.empty(M, K), mg.GatedWork.empty(ffn, M)
+    rng = np.random.default_rng(M)
+    x, xs = rows(rng, M, K).contiguous(), [rows(rng, M, K).contiguous() for _ in range(4)]
+    y, z = (torch.empty(M, n, dtype=torch.bfloat16, device="cuda") for n in (F, N))
+
+    def step(a, b):
+        mg.f8_forward(plan, x, act=act, Y=a)
+        mg.gated_ffn_forward(ffn, x, Y=b, work=work)
+
+    step(y, z)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        step(y, z)
+    want = []
+    for v in xs:
+        x.copy_(v)
+        a, b = torch.empty_like(y), torch.empty_like(z)
+        step(a, b)
+        want.append((v, a, b))
+    for v, a, b in want + want[:2]:
+        x.copy_(v)
+        y.fill_(float("nan")), z.fill_(float("nan"))
+        g.replay()
+        step(torch.empty_like(y), torch.empty_like(z))
+        torch.cuda.synchronize()
+        assert torch.equal(y, a) and torch.equal(z, b)
