@@ -268,7 +268,7 @@ bool f8_direct_pays(int64_t M, int32_t K, int32_t N) {
 // steps apart: 5120 -> 13824 -> 5120 1 row 47.0, 49.9; 3 rows 48.8, 50.6; 4 rows 51.0, 50.6; 1024
 // -> 4096 -> 1024 9 rows 17.1, 17.3; 13 rows 19.5, 17.4; 5120 -> 5120 -> 5120 5 rows 27.2, 26.6; 7 rows
 // 30.0, 26.9; 5120 -> 1024 -> 5120 11 rows 22.3, 18.7; 2048 -> 2048 -> 55296 3 rows 31.3, 34.3; 16 rows
-// 50.0, 36.0.  Of 70 such blocks the rule takes the slower form, by 9 %, at 5120
+// 50.0, 36.0.  Of 71 such blocks the rule takes the slower form, by 9 %, at 5120
 // -> 1024 -> 5120 8 rows, and by 2 % at most elsewhere.
 bool f8_direct_pays_gated(int64_t M, int32_t K, int32_t F, int32_t N) {
     const int64_t units = f8_slices(K) / 4 + f8_slices(F) / 4;
